@@ -316,6 +316,66 @@ esd_status esd_partial_attention(esd_ctx* ctx, const void* q, const void* k_cach
                                  const void* v_cache, int B, int L, int k, void* out,
                                  void* stream);
 
+/* Key/value cache in 4 bits (no counterpart in the papers: it holds the K and V
+ * of the partial cache in about a quarter of the bytes, for long contexts and
+ * large batches). Memory owned by the caller, 16-byte aligned:
+ *  k_codes, v_codes   uint32 [B, capacity, n_kv_heads, head_dim / 8]: 4-bit
+ *    codes, dim 2i of a word's eight in bits 4i..4i+3, dim 2i+1 in bits
+ *    16+4i..16+4i+3;
+ *  k_scales, v_scales bf16 [B, capacity, n_kv_heads, head_dim / group, 2]: the
+ *    step s and the offset z of every group of `group` consecutive dims.
+ * Row i of sequence b (position i) is row b*capacity + i. Dims of a group read
+ * back as (16 + c) s + z, rounded once to the storage type. group is 32, 64 or
+ * 128 and divides head_dim (itself a multiple of 32); n_kv_heads divides the
+ * model's n_heads: query heads h n_heads/n_kv_heads .. (h + 1) n_heads/n_kv_heads
+ * - 1 share key/value head h. */
+typedef struct {
+  void* k_codes;
+  void* v_codes;
+  void* k_scales;
+  void* v_scales;
+  int n_kv_heads;
+  int capacity;  /* rows per sequence */
+  int group;     /* dims that share a step and an offset */
+} esd_kv_quant;
+
+/* Write rows into the 4-bit cache: row b*n + j of k and v ([B*n, n_kv_heads *
+ * head_dim], storage type, RoPE already applied to k) goes to position
+ * idx[b, j] of sequence b (int32 [B, n]; NULL: position j, n <= capacity).
+ * A negative entry marks a padding row, of which nothing is written; entries
+ * of a sequence are distinct (a position given twice holds either row, or
+ * heads of both). Per group with extremes lo and hi, in float32 steps:
+ *   t = (hi - lo) / 15,  z = lo - 16 t rounded down to bf16,
+ *   s = (hi - z) / 31 rounded to bf16,
+ *   c = the whole number nearest to (x - (16 s + z)) / s (the quotient exact,
+ *       ties to even), clamped to 0..15; 0 where s is 0.
+ * A group that holds a NaN or an infinity, or whose span overflows, gets
+ * s = z = NaN and reads back as NaN. Rows that the call does not name stay as
+ * they are. A position at or past the capacity is skipped and reported as
+ * ESD_ERR_CHECK by the next esd_sync_check. Requires B <= max_batch,
+ * 1 <= n <= max_len; k and v 16-byte aligned, apart from the cache. */
+esd_status esd_kv_quantize(esd_ctx* ctx, const void* k, const void* v, const int32_t* idx, int B,
+                           int n, const esd_kv_quant* cache, void* stream);
+
+/* Read rows of the 4-bit cache back: k_out and v_out [B*n, n_kv_heads *
+ * head_dim] (storage type, 16-byte aligned), positions as for esd_kv_quantize.
+ * The rows of negative or out-of-range positions are zeros (the latter also
+ * reported as ESD_ERR_CHECK by the next esd_sync_check). */
+esd_status esd_kv_dequantize(esd_ctx* ctx, const esd_kv_quant* cache, const int32_t* idx, int B,
+                             int n, void* k_out, void* v_out, void* stream);
+
+/* esd_partial_attention over a 4-bit cache: out[b*k + j] = softmax(q[b*k + j]
+ * K_b^T / sqrt(head_dim)) V_b per head, K_b and V_b the first L rows of
+ * sequence b as esd_kv_dequantize reads them back. lens (device int32 [B], may
+ * be NULL): sequence b has min(lens[b], L) keys; rows behind them are not
+ * attended to, whatever the cache holds there, and the outputs of a sequence
+ * without keys are zeros. q, out: [B*k, d] (RoPE already applied to q), 16-byte
+ * aligned, not overlapping. Requires B <= max_batch, 1 <= L <= max_len,
+ * L <= capacity, 1 <= k <= max_len. */
+esd_status esd_partial_attention_quantized(esd_ctx* ctx, const void* q, const esd_kv_quant* cache,
+                                           const int32_t* lens, int B, int L, int k, void* out,
+                                           void* stream);
+
 /* Head: final RMSNorm, vocabulary projection, softmax maximum and argmax
  * ([ES] section 2.A: c is the maximum probability) of rows x_rows [B*k, d].
  * The mask id is excluded from the softmax and the argmax; argmax ties go to

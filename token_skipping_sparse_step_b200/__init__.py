@@ -40,7 +40,8 @@ EXPORTS = ("esd_create", "esd_destroy", "esd_last_error", "esd_keep_count", "esd
            "esd_partial_attention", "esd_context_saliency", "esd_dyllm_layers_forward",
            "esd_dyllm_layers_forward_approx",
            "esd_selftest_wait_timeout", "esd_approx_attention", "esd_noalloc_check",
-           "esd_noalloc_selftest_wait_timeout")
+           "esd_noalloc_selftest_wait_timeout", "esd_kv_quantize", "esd_kv_dequantize",
+           "esd_partial_attention_quantized")
 K_GEMM_QKV, K_GEMM_O, K_GEMM_GATE_UP, K_GEMM_DOWN, K_HEAD, K_ATTENTION, K_SCORE_SELECT = 0, 1, 2, 3, 4, 6, 7
 
 
@@ -74,6 +75,12 @@ class StateView(ctypes.Structure):
                 ("max_len", ctypes.c_int)]
 
 
+class _KVQuantView(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("n_kv_heads", ctypes.c_int), ("capacity", ctypes.c_int),
+                ("group", ctypes.c_int)]
+
+
 _vp, _i, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
 _sigs = {
     "esd_create": [ctypes.POINTER(ModelDims), ctypes.POINTER(Weights), ctypes.POINTER(RunConfig),
@@ -92,6 +99,9 @@ _sigs = {
     "esd_sparse_layers_forward": [_vp, _i, _i, _vp, _i, _i, _i, _vp, _vp],
     "esd_confidence_argmax": [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp],
     "esd_partial_attention": [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp],
+    "esd_kv_quantize": [_vp, _vp, _vp, _vp, _i, _i, ctypes.POINTER(_KVQuantView), _vp],
+    "esd_kv_dequantize": [_vp, ctypes.POINTER(_KVQuantView), _vp, _i, _i, _vp, _vp, _vp],
+    "esd_partial_attention_quantized": [_vp, _vp, ctypes.POINTER(_KVQuantView), _vp, _i, _i, _i, _vp, _vp],
     "esd_logits": [_vp, _vp, _i, _vp, _vp],
     "esd_remask": [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp],
     "esd_denoise_step": [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp],
@@ -148,6 +158,47 @@ class _CudaView:
 
 
 _TYPESTR = {torch.float32: "<f4", torch.int32: "<i4"}
+
+
+class KVQuant:
+    """A 4-bit key/value cache (``esd_kv_quant``) over the caller's tensors,
+    kept alive by it: codes int32 [B, capacity, n_kv_heads, head_dim / 8] and
+    scales bfloat16 [B, capacity, n_kv_heads, head_dim / group, 2], contiguous
+    CUDA tensors of one device, for the keys and for the values."""
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales, head_dim: int):
+        if k_codes.dim() != 4 or k_scales.dim() != 5 or head_dim % 32 or k_codes.shape[3] * 8 != head_dim:
+            raise ValueError("codes are [B, capacity, n_kv_heads, head_dim / 8], "
+                             "scales [B, capacity, n_kv_heads, head_dim / group, 2], head_dim a multiple of 32")
+        groups = k_scales.shape[3]
+        if groups < 1 or head_dim % groups or head_dim // groups not in (32, 64, 128):
+            raise ValueError("a group holds 32, 64 or 128 dims and divides head_dim")
+        if tuple(k_scales.shape) != (*k_codes.shape[:3], groups, 2):
+            raise ValueError("the scales' shape does not go with the codes'")
+        for codes, scales in ((k_codes, k_scales), (v_codes, v_scales)):
+            if codes.dtype != torch.int32 or scales.dtype != torch.bfloat16:
+                raise ValueError("codes are int32, scales bfloat16")
+            if codes.shape != k_codes.shape or scales.shape != k_scales.shape:
+                raise ValueError("keys and values have the same shapes")
+            for t in (codes, scales):
+                if not t.is_contiguous() or t.device != k_codes.device:
+                    raise ValueError("contiguous tensors of one device")
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.batch, self.capacity, self.n_kv_heads = k_codes.shape[:3]
+        self.head_dim, self.group = head_dim, head_dim // groups
+        self._view = _KVQuantView(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                                  self.n_kv_heads, self.capacity, self.group)
+        self._ref = ctypes.byref(self._view)
+
+    @classmethod
+    def empty(cls, batch: int, capacity: int, n_kv_heads: int, head_dim: int, group: int = 64, device="cuda"):
+        """A cache whose every value reads back as zero."""
+        if group not in (32, 64, 128) or head_dim % group:
+            raise ValueError("a group holds 32, 64 or 128 dims and divides head_dim")
+        codes = lambda: torch.zeros(batch, capacity, n_kv_heads, head_dim // 8, dtype=torch.int32, device=device)
+        scales = lambda: torch.zeros(batch, capacity, n_kv_heads, head_dim // group, 2, dtype=torch.bfloat16,
+                                     device=device)
+        return cls(codes(), codes(), scales(), scales(), head_dim)
 
 
 class Context:
@@ -282,6 +333,47 @@ class Context:
     def partial_attention(self, q, k_cache, v_cache, B, L, k, out, stream=None):
         self._check(_lib.esd_partial_attention(self.handle, _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                                B, L, k, _ptr(out), _stream(stream)))
+
+    def _check_rows(self, cache, B, what, *tensors):
+        """The tensors of a 4-bit cache call: storage type, contiguous and large enough for the kernels."""
+        if cache.head_dim != self.dims.head_dim or B > cache.batch:
+            raise ValueError("the cache has %d sequences of head_dim %d" % (cache.batch, cache.head_dim))
+        dt = self.storage_dtype
+        for t, rows, width in tensors:
+            if t.dtype != dt or not t.is_contiguous() or t.numel() < rows * width or not t.is_cuda:
+                raise ValueError("%s: contiguous %s CUDA tensors of at least %d x %d" % (what, dt, rows, width))
+
+    @staticmethod
+    def _check_i32(t, n, what):
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n or not t.is_cuda):
+            raise ValueError("%s: a contiguous int32 CUDA tensor of at least %d" % (what, n))
+
+    def kv_quantize(self, k, v, idx, B, n, cache: KVQuant, stream=None):
+        """Write rows k, v [B*n, n_kv_heads * head_dim] at positions idx [B, n]
+        (None: 0 .. n - 1) of a 4-bit cache; see esd_kv_quantize."""
+        w = cache.n_kv_heads * cache.head_dim
+        self._check_rows(cache, B, "k, v", (k, B * n, w), (v, B * n, w))
+        self._check_i32(idx, B * n, "idx")
+        self._check(_lib.esd_kv_quantize(self.handle, _ptr(k), _ptr(v), _ptr(idx), B, n, cache._ref, _stream(stream)))
+
+    def kv_dequantize(self, cache: KVQuant, idx, B, n, k_out, v_out, stream=None):
+        """Read rows at positions idx [B, n] (None: 0 .. n - 1) of a 4-bit cache
+        back into k_out, v_out; see esd_kv_dequantize."""
+        w = cache.n_kv_heads * cache.head_dim
+        self._check_rows(cache, B, "k_out, v_out", (k_out, B * n, w), (v_out, B * n, w))
+        self._check_i32(idx, B * n, "idx")
+        self._check(_lib.esd_kv_dequantize(self.handle, cache._ref, _ptr(idx), B, n, _ptr(k_out), _ptr(v_out),
+                                           _stream(stream)))
+
+    def partial_attention_quantized(self, q, cache: KVQuant, B, L, k, out, lens=None, stream=None):
+        """Attention of q [B*k, d] over the first L rows of a 4-bit cache (of
+        sequence b the first lens[b], int32 [B]); see
+        esd_partial_attention_quantized."""
+        d = self.dims.d
+        self._check_rows(cache, B, "q, out", (q, B * k, d), (out, B * k, d))
+        self._check_i32(lens, B, "lens")
+        self._check(_lib.esd_partial_attention_quantized(self.handle, _ptr(q), cache._ref, _ptr(lens), B, L, k,
+                                                         _ptr(out), _stream(stream)))
 
     def confidence_argmax(self, x_rows, idx, B, L, k, conf_out, tok_out, stream=None):
         self._check(_lib.esd_confidence_argmax(self.handle, _ptr(x_rows), _ptr(idx), B, L, k,

@@ -29,6 +29,7 @@
 #include "attention_mma.cuh"
 #include "attention_pair.cuh"
 #include "approx_attention.cuh"
+#include "attention_quant.cuh"
 
 using esd::HeadPartial;
 using esd::StepParams;
@@ -560,6 +561,73 @@ esd_status k_score_select(esd_ctx* c, const void* x, const void* h, const float*
   ESD_LAUNCHED(c);
   esd::topk_kernel<<<B, esd::kTopkThreads, (size_t)L * sizeof(uint32_t), st>>>(scores, L, k, idx);
   ESD_LAUNCHED(c);
+  return ESD_OK;
+}
+
+// The 4-bit cache of a call, checked against the context's head geometry.
+esd_status check_kv(esd_ctx* c, const esd_kv_quant* kv, esd::KvQuant* out) {
+  if (!kv || !kv->k_codes || !kv->v_codes || !kv->k_scales || !kv->v_scales)
+    return fail(c, ESD_ERR_INVALID_ARG, "null pointer");
+  const uintptr_t codes = (uintptr_t)kv->k_codes | (uintptr_t)kv->v_codes;
+  const uintptr_t scales = (uintptr_t)kv->k_scales | (uintptr_t)kv->v_scales;
+  if ((codes & 15) || (scales & 15)) return fail(c, ESD_ERR_INVALID_ARG, "cache pointers need 16-byte alignment");
+  const int H = c->dims.n_heads, hd = c->dims.head_dim, g = kv->group;
+  if (g != 32 && g != 64 && g != 128) return fail(c, ESD_ERR_INVALID_ARG, "group %d is not 32, 64 or 128", g);
+  if (hd % 32) return fail(c, ESD_ERR_UNSUPPORTED, "head_dim %d is not a multiple of 32", hd);
+  if (hd % g) return fail(c, ESD_ERR_INVALID_ARG, "group %d does not divide head_dim %d", g, hd);
+  if (kv->n_kv_heads < 1 || H % kv->n_kv_heads)
+    return fail(c, ESD_ERR_INVALID_ARG, "%d key/value heads do not divide %d heads", kv->n_kv_heads, H);
+  if (kv->capacity < 1) return fail(c, ESD_ERR_INVALID_ARG, "capacity %d", kv->capacity);
+  int dev = -1;
+  ESD_CUDA(c, cudaGetDevice(&dev));
+  if (dev != c->device)
+    return fail(c, ESD_ERR_INVALID_ARG, "the context is on device %d, the current device is %d", c->device, dev);
+  *out = esd::KvQuant{(uint32_t*)kv->k_codes, (uint32_t*)kv->v_codes, (uint32_t*)kv->k_scales, (uint32_t*)kv->v_scales,
+                      kv->n_kv_heads, kv->capacity, g == 32 ? 5 : g == 64 ? 6 : 7};
+  return ESD_OK;
+}
+
+// B sequences of n rows against a cache: positions 0 .. n - 1 without idx.
+esd_status check_kv_rows(esd_ctx* c, const esd::KvQuant& kv, const int32_t* idx, int B, int n, const void* k,
+                         const void* v) {
+  ESD_TRY(check_bl(c, B, n));
+  if (!k || !v) return fail(c, ESD_ERR_INVALID_ARG, "null pointer");
+  if (((uintptr_t)k | (uintptr_t)v) & 15) return fail(c, ESD_ERR_INVALID_ARG, "rows need 16-byte alignment");
+  if (!idx && n > kv.capacity)
+    return fail(c, ESD_ERR_INVALID_ARG, "%d rows do not fit the capacity %d", n, kv.capacity);
+  return ESD_OK;
+}
+
+template <typename T>
+esd_status k_kv_quantize(esd_ctx* c, const void* k, const void* v, const int32_t* idx, int B, int n,
+                         const esd::KvQuant& kv, cudaStream_t st) {
+  const int per_row = kv.n_kv * (c->dims.head_dim / 16);
+  const long long total = (long long)B * n * per_row;
+  esd::kv_quantize_kernel<T><<<dim3(cdiv(total, 256), 2), 256, 0, st>>>((const T*)k, (const T*)v, idx, total, n,
+                                                                        per_row, kv, c->flag);
+  ESD_LAUNCHED(c);
+  return ESD_OK;
+}
+
+template <typename T>
+esd_status k_kv_dequantize(esd_ctx* c, const esd::KvQuant& kv, const int32_t* idx, int B, int n, void* k, void* v,
+                           cudaStream_t st) {
+  const int per_row = kv.n_kv * (c->dims.head_dim / 8);
+  const long long total = (long long)B * n * per_row;
+  esd::kv_dequantize_kernel<T><<<dim3(cdiv(total, 256), 2), 256, 0, st>>>(kv, idx, total, n, per_row, (T*)k, (T*)v,
+                                                                          c->flag);
+  ESD_LAUNCHED(c);
+  return ESD_OK;
+}
+
+template <typename T>
+esd_status k_attention_quant(esd_ctx* c, const void* Q, const esd::KvQuant& kv, const int32_t* lens, void* O, int B,
+                             int n, int L, cudaStream_t st) {
+  const int share = c->dims.n_heads / kv.n_kv;
+  ProfScope ps(c, ESD_K_ATTENTION, B * n, st);
+  const cudaError_t e = esd::quant_attention_simt<T>(Q, kv, lens, O, B, n, L, share, c->dims.head_dim, c->tc.num_sms, st);
+  c->launches++;
+  if (e != cudaSuccess) return fail(c, ESD_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
   return ESD_OK;
 }
 
@@ -1338,7 +1406,9 @@ esd_status esd_create(const esd_model_dims* dims, const esd_weights* w, const es
       return ESD_ERR_CUDA;
     }
   }
-  if (cudaDeviceSynchronize() != cudaSuccess) {
+  if ((c->bf16 ? esd::quant_attention_simt_setup<__nv_bfloat16>(m.head_dim)
+               : esd::quant_attention_simt_setup<float>(m.head_dim)) != cudaSuccess ||
+      cudaDeviceSynchronize() != cudaSuccess) {
     free_all(c);
     delete c;
     return ESD_ERR_CUDA;
@@ -1557,6 +1627,49 @@ esd_status esd_partial_attention(esd_ctx* c, const void* q, const void* kc, cons
   cudaStream_t st = (cudaStream_t)stream;
   if (c->bf16) return k_attention<__nv_bfloat16>(c, q, kc, vc, out, B * k, k, L, st);
   return k_attention<float>(c, q, kc, vc, out, B * k, k, L, st);
+}
+
+esd_status esd_kv_quantize(esd_ctx* c, const void* k, const void* v, const int32_t* idx, int B, int n,
+                           const esd_kv_quant* cache, void* stream) {
+  if (!c) return ESD_ERR_INVALID_ARG;
+  c->err.clear();
+  esd::KvQuant kv;
+  ESD_TRY(check_kv(c, cache, &kv));
+  ESD_TRY(check_kv_rows(c, kv, idx, B, n, k, v));
+  cudaStream_t st = (cudaStream_t)stream;
+  return c->bf16 ? k_kv_quantize<__nv_bfloat16>(c, k, v, idx, B, n, kv, st)
+                 : k_kv_quantize<float>(c, k, v, idx, B, n, kv, st);
+}
+
+esd_status esd_kv_dequantize(esd_ctx* c, const esd_kv_quant* cache, const int32_t* idx, int B, int n, void* k_out,
+                             void* v_out, void* stream) {
+  if (!c) return ESD_ERR_INVALID_ARG;
+  c->err.clear();
+  esd::KvQuant kv;
+  ESD_TRY(check_kv(c, cache, &kv));
+  ESD_TRY(check_kv_rows(c, kv, idx, B, n, k_out, v_out));
+  cudaStream_t st = (cudaStream_t)stream;
+  return c->bf16 ? k_kv_dequantize<__nv_bfloat16>(c, kv, idx, B, n, k_out, v_out, st)
+                 : k_kv_dequantize<float>(c, kv, idx, B, n, k_out, v_out, st);
+}
+
+esd_status esd_partial_attention_quantized(esd_ctx* c, const void* q, const esd_kv_quant* cache, const int32_t* lens,
+                                           int B, int L, int k, void* out, void* stream) {
+  if (!c) return ESD_ERR_INVALID_ARG;
+  c->err.clear();
+  ESD_TRY(check_bl(c, B, L));
+  if (k < 1 || k > c->run.max_len)
+    return fail(c, ESD_ERR_INVALID_ARG, "k = %d outside [1, %d]", k, c->run.max_len);
+  if (!q || !out) return fail(c, ESD_ERR_INVALID_ARG, "null pointer");
+  if (((uintptr_t)q | (uintptr_t)out) & 15)
+    return fail(c, ESD_ERR_INVALID_ARG, "q and out need 16-byte alignment");
+  esd::KvQuant kv;
+  ESD_TRY(check_kv(c, cache, &kv));
+  if (L > kv.capacity) return fail(c, ESD_ERR_INVALID_ARG, "length %d above the capacity %d", L, kv.capacity);
+  if ((long long)B * kv.n_kv > 65535) return fail(c, ESD_ERR_UNSUPPORTED, "grid limits");
+  cudaStream_t st = (cudaStream_t)stream;
+  return c->bf16 ? k_attention_quant<__nv_bfloat16>(c, q, kv, lens, out, B, k, L, st)
+                 : k_attention_quant<float>(c, q, kv, lens, out, B, k, L, st);
 }
 
 esd_status esd_confidence_argmax(esd_ctx* c, const void* x_rows, const int32_t* idx, int B, int L,
