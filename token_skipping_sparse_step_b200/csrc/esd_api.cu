@@ -30,6 +30,7 @@
 #include "attention_pair.cuh"
 #include "approx_attention.cuh"
 #include "attention_quant.cuh"
+#include "attention_quant_rows.cuh"
 
 using esd::HeadPartial;
 using esd::StepParams;
@@ -625,7 +626,12 @@ esd_status k_attention_quant(esd_ctx* c, const void* Q, const esd::KvQuant& kv, 
                              int n, int L, cudaStream_t st) {
   const int share = c->dims.n_heads / kv.n_kv;
   ProfScope ps(c, ESD_K_ATTENTION, B * n, st);
-  const cudaError_t e = esd::quant_attention_simt<T>(Q, kv, lens, O, B, n, L, share, c->dims.head_dim, c->tc.num_sms, st);
+  const int sms = c->tc.num_sms;
+  cudaError_t e;
+  if (sizeof(T) == 2 && n <= 16 && n * share <= 16)
+    e = esd::quant_attention_rows(Q, kv, lens, O, B, n, L, share, sms, st);
+  else
+    e = esd::quant_attention_simt<T>(Q, kv, lens, O, B, n, L, share, c->dims.head_dim, sms, st);
   c->launches++;
   if (e != cudaSuccess) return fail(c, ESD_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
   return ESD_OK;
@@ -1408,7 +1414,7 @@ esd_status esd_create(const esd_model_dims* dims, const esd_weights* w, const es
   }
   if ((c->bf16 ? esd::quant_attention_simt_setup<__nv_bfloat16>(m.head_dim)
                : esd::quant_attention_simt_setup<float>(m.head_dim)) != cudaSuccess ||
-      cudaDeviceSynchronize() != cudaSuccess) {
+      (c->bf16 && esd::quant_attention_rows_setup() != cudaSuccess) || cudaDeviceSynchronize() != cudaSuccess) {
     free_all(c);
     delete c;
     return ESD_ERR_CUDA;

@@ -60,7 +60,10 @@ __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t 
 // the codes of dims 2i and 2i + 1 of a word as the bf16 numbers 16 + c
 __device__ __forceinline__ uint32_t kv_code_pair(uint32_t w, int i) {
   const uint32_t x = i == 0 ? w << 3 : w >> (4 * i - 3);
-  return (x & 0x00780078u) | 0x41804180u;
+  uint32_t r;
+  // one mask-and-or (written out, or the two constants become two operations)
+  asm("lop3.b32 %0, %1, 0x00780078, 0x41804180, 0xEA;" : "=r"(r) : "r"(x));
+  return r;
 }
 
 // The eight values of a word. ss, zz: the step and the offset in both halves
