@@ -31,6 +31,7 @@
 #include "approx_attention.cuh"
 #include "attention_quant.cuh"
 #include "attention_quant_rows.cuh"
+#include "attention_quant_tc.cuh"
 
 using esd::HeadPartial;
 using esd::StepParams;
@@ -630,6 +631,8 @@ esd_status k_attention_quant(esd_ctx* c, const void* Q, const esd::KvQuant& kv, 
   cudaError_t e;
   if (sizeof(T) == 2 && n <= 16 && n * share <= 16)
     e = esd::quant_attention_rows(Q, kv, lens, O, B, n, L, share, sms, st);
+  else if (sizeof(T) == 2)
+    e = esd::quant_attention_tc(Q, kv, lens, O, B, n, L, share, sms, c->flag, st);
   else
     e = esd::quant_attention_simt<T>(Q, kv, lens, O, B, n, L, share, c->dims.head_dim, sms, st);
   c->launches++;
@@ -1414,7 +1417,7 @@ esd_status esd_create(const esd_model_dims* dims, const esd_weights* w, const es
   }
   if ((c->bf16 ? esd::quant_attention_simt_setup<__nv_bfloat16>(m.head_dim)
                : esd::quant_attention_simt_setup<float>(m.head_dim)) != cudaSuccess ||
-      (c->bf16 && esd::quant_attention_rows_setup() != cudaSuccess) || cudaDeviceSynchronize() != cudaSuccess) {
+      (c->bf16 && (esd::quant_attention_rows_setup() != cudaSuccess || esd::quant_attention_tc_setup() != cudaSuccess)) || cudaDeviceSynchronize() != cudaSuccess) {
     free_all(c);
     delete c;
     return ESD_ERR_CUDA;
