@@ -4,23 +4,29 @@
 //
 // A CTA takes one key/value head of one sequence, a slice of its keys, and query
 // rows (row i: query i / share, head kvh share + i % share) in two streams of 128
-// rows, TMEM lane = row. More than 128 rows: the streams are two row tiles, and
+// lanes (TMEM lane = row). More than 128 rows: the streams are two row tiles, and
 // each chunk serves both. Up to 128: the streams are the even and the odd chunks of
-// the same rows, each with sums and an accumulator of its own, merged at the end;
-// up to 64 rows the odd stream's rows lie in lanes 64 and up, so that the softmax
-// of the two streams runs on different schedulers. Two streams keep the tensor
-// cores at work: while one stream's scores go through the softmax, the other's
-// products run.
+// the same rows, each with sums and an accumulator of its own. Two streams keep the
+// tensor cores at work: while one's scores go through the softmax, the other's
+// products run. Up to 64 (32) rows, 2 (4) copies of a row lie in the 128 lanes, and
+// each copy takes a half (quarter) of every chunk's keys, with P zero at the
+// others: the products cost the same, the softmax is spread over all its warps.
+// Streams and copies are merged at the end.
 //
-// Warps: 0..3 and 4..7 the softmax of streams 0 and 1 (thread = row: no exchange
-// between threads); 8..15 expand codes: the next chunk's codes, steps and offsets
-// are in registers while the current one becomes bf16 K and V tiles, [128 keys][64
-// dims] x 2 in the 128-byte swizzle that TMA would write (K: K-major operand, V:
-// MN-major); a warp's lanes are laid out so that its 16-byte stores are free of
-// bank conflicts. 16 issues the MMAs: per stream S = Q K^T (M 128, N 128 keys, K
-// 128 dims) into TMEM, then O += P V with P (bf16) read from TMEM, where the
-// softmax wrote it over the scores that it came from. S of a stream's next chunk is
-// issued once its P V is done.
+// Warps: 0..3 and 4..7 the softmax of streams 0 and 1 (thread = lane: no exchange
+// between threads, a row's scores in registers). A stream is a chain: S = Q K^T (M
+// 128, N 128 keys, K 128 dims) into TMEM, softmax, P (bf16) into TMEM over the
+// scores that it came from, O += P V with P read from there, the next S. So its
+// first warp issues its MMAs too, in the time in which it would wait for them (one
+// thread that issues for both and polls for what can go took 1.4x the time: it
+// stands still while an MMA is queued). 8..15 expand codes, each the same 16 rows of
+// K and of V in every chunk, which it copies itself by TMA through a ring of its own
+// (no other warp waits on it; registers as the ring kept too few bytes in flight:
+// 1.65 us a chunk), the steps and offsets two or three chunks ahead in registers:
+// bf16 tiles [128 keys][64 dims] x 2 in the 128-byte swizzle that TMA would write (K:
+// K-major operand, V: MN-major); a warp's lanes are laid out so that its 16-byte
+// stores are free of bank conflicts. Without copies the softmax warps take registers
+// from these (setmaxnreg).
 //
 // The running maximum moves only when a chunk's exceeds it by more than 2^8 (O is
 // then scaled in TMEM; the result O / l is the same). P is rounded to bf16 for its
@@ -38,25 +44,22 @@ namespace esd {
 constexpr int kAtRows = 128, kAtKeys = 128, kAtHd = 128;
 constexpr int kAtBox = 128 * 64 * 2;              // 128 rows x 64 dims
 constexpr int kAtTile = 2 * kAtBox;               // Q of a stream, K or V of a chunk
-constexpr int kAtConv = 256, kAtThreads = 256 + kAtConv + 32;
+// registers a thread: at launch, then (without copies: a copy's share of a row's scores leaves room as it is)
+constexpr int kAtRegs = 128, kAtSoftRegs = 176, kAtOtherRegs = 80;
+static_assert(kAtSoftRegs + kAtOtherRegs <= 2 * kAtRegs, "half of the threads each");
 constexpr int kAtLd = kAtHd + 4;                  // floats of a merge row
-constexpr int kAtMain = 2 * kAtTile + 4 * kAtTile;  // Q, K ring, V ring
-constexpr int kAtStats = 2 * 2 * kAtRows * 4;     // merge: row maxima and sums of both streams
-constexpr int kAtSmem = kAtMain + kAtStats + 256 + 1024;
+constexpr int kAtConv = 8, kAtThreads = 512;  // expanding warps
+constexpr int kAtRaw = kAtConv * 2 * 16 * 64;       // a chunk's codes: per warp 16 rows of K, 16 of V
+constexpr int kAtStats = 2 * 2 * kAtRows * 4;     // merge: row maxima and sums of both streams (over the raw ring)
+// Q, the K and V stages, the raw ring
+constexpr int at_stages(bool two) { return two ? 2 : 3; }
+constexpr int at_main(bool two) { return ((two ? 2 : 1) + 4) * kAtTile; }
+constexpr int at_smem(bool two) { return at_main(two) + at_stages(two) * kAtRaw + 512 + 1024; }
 constexpr int kAtMaxSplits = 8;
-static_assert(2 * kAtRows * kAtLd * 4 <= kAtMain, "the merge rows lie over the tiles");
+static_assert(2 * kAtRows * kAtLd * 4 <= at_main(false), "the merge rows lie over the tiles");
+static_assert(kAtStats <= 2 * kAtRaw, "the merge statistics lie over the raw ring");
+static_assert(at_smem(true) <= 232448 && at_smem(false) <= 232448, "227 KB");
 
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // D (+)= A B with A in tensor memory (lane = row, two bf16 per column)
 __device__ __forceinline__ void tc_mma_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
                                           uint32_t accumulate) {
@@ -83,256 +86,317 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// A thread's share of a chunk: rows r and r + 64 of K and of V, 32 dims each.
-struct AtRaw {
-  uint4 k[2], v[2];
-  uint32_t ks[2], vs[2];
-};
+// packed pairs of float32
+__device__ __forceinline__ uint64_t pack_f2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack_f2(uint64_t a, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_f4(uint32_t addr, float x, float y, float z, float w) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
+}
 
-// Grid (tiles * splits, B * n_kv), cluster (splits). TWO: two row tiles per CTA;
-// else one (rows <= 128).
-template <bool TWO>
+// A warp's wait, polled by one lane: 32 lanes that poll take the barrier unit from
+// the warps that arrive.
+__device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* flag) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, flag);
+  __syncwarp();
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Grid (tiles * splits, B * n_kv), cluster (splits). TWO: two row tiles per CTA
+// (NSUB 1); else one of at most 128 / NSUB rows, in NSUB copies.
+template <bool TWO, int NSUB>
 __global__ void __launch_bounds__(kAtThreads, 1)
-quant_attention_tc_kernel(const __nv_bfloat16* __restrict__ Q, KvQuant cache, const int32_t* __restrict__ lens,
+quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                          const __nv_bfloat16* __restrict__ Q, KvQuant cache, const int32_t* __restrict__ lens,
                           __nv_bfloat16* __restrict__ O, int n, int L, int share, int splits, float scale_log2,
                           int* flag) {
+  static_assert(!TWO || NSUB == 1, "copies only of one tile");
+  constexpr bool kTurns = TWO;
+  constexpr bool kSplitRegs = NSUB == 1;
+  constexpr int kStages = at_stages(TWO);
+  constexpr int kPad = kAtRows / NSUB, kPer = kAtKeys / NSUB;  // lanes of a copy, its keys of a chunk
   extern __shared__ __align__(1024) uint8_t smem_at_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_at_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t* sQ = smem;                  // [stream][dims 0-63 | 64-127][128 rows]
-  uint8_t* sK = sQ + 2 * kAtTile;      // [stage][...][128 keys]
-  uint8_t* sV = sK + 2 * kAtTile;
-  float* s_m = reinterpret_cast<float*>(sV + 2 * kAtTile);  // [stream][128]
+  const uint32_t base = (smem_u32(smem_at_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_at_raw + (base - smem_u32(smem_at_raw));
+  const uint32_t aQ = base;                 // [stream (TWO)][dims 0-63 | 64-127][128 rows]
+  const uint32_t aK = aQ + (TWO ? 2 : 1) * kAtTile;  // [stage][...][128 keys]
+  const uint32_t aV = aK + 2 * kAtTile;
+  const uint32_t aRaw = base + at_main(TWO);         // [warp][stage][16 rows of K | of V]
+  float* s_m = reinterpret_cast<float*>(smem + at_main(TWO));  // [stream][128], over the ring
   float* s_l = s_m + 2 * kAtRows;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_l + 2 * kAtRows);
-  uint64_t* qfull = bars;         // Q written
-  uint64_t* kfull = bars + 1;     // [2] K of a chunk written
-  uint64_t* vfull = bars + 3;     // [2]
-  uint64_t* kempty = bars + 5;    // [2] the scores that read it are done
-  uint64_t* vempty = bars + 7;    // [2]
-  uint64_t* sfull = bars + 9;     // [2] a stream's scores in TMEM
-  uint64_t* pready = bars + 11;   // [2] a stream's P written, its O scaled
-  uint64_t* pvdone = bars + 13;   // [2] a stream's P V accumulated
-  uint64_t* drain = bars + 15;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
+  const uint32_t bars = aRaw + kStages * kAtRaw;
+  const uint32_t qfull = bars;          // Q written
+  const uint32_t kfull = bars + 8;      // [2] K of a chunk written
+  const uint32_t vfull = bars + 24;     // [2]
+  const uint32_t kempty = bars + 40;    // [2] the scores that read it are done
+  const uint32_t vempty = bars + 56;    // [2]
+  const uint32_t sfull = bars + 72;     // [2] a stream's scores in TMEM
+  const uint32_t pready = bars + 88;    // [2] a stream's P written, its O scaled
+  const uint32_t pvdone = bars + 104;   // [2] a stream's P V accumulated
+  const uint32_t drain = bars + 120;    // [2] a stream's MMAs, all of them
+  const uint32_t turn = bars + 136;     // [2] the stream may take its exponentials
+  const uint32_t rawfull = bars + 152;  // [warp][stage] a warp's codes have landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars - base) + 152 + kAtConv * kStages * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x % splits, tile = blockIdx.x / splits;
   const int b = blockIdx.y / cache.n_kv, kvh = blockIdx.y % cache.n_kv;
-  const int H = cache.n_kv * share, r0 = tile * (TWO ? 256 : 128);
-  const int rows = min(n * share - r0, TWO ? 256 : 128);  // rows of this CTA
-  const int shift = !TWO && rows <= 64 ? 64 : 0;          // lanes between a row of the two streams
+  const int H = cache.n_kv * share, r0 = tile * 256;
+  const int rows = min(n * share - r0, TWO ? 256 : kPad);  // rows of this CTA
   const int len = lens ? min(L, max(0, lens[b])) : L;
   const int chunks = (len + kAtKeys - 1) / kAtKeys;
-  const int c0 = (int)((long long)chunks * split / splits), nc = (int)((long long)chunks * (split + 1) / splits) - c0;
+  const int c0 = chunks * split / splits, nc = chunks * (split + 1) / splits - c0;
 
+  const int streams = TWO && rows <= kAtRows ? 1 : 2;
+
+  // 16 rows of codes of chunk j into the warp's stage j % kStages
+  auto copy = [&](int j) {
+    const int w = warp - 8, st = j % kStages, row = b * cache.capacity + (c0 + j) * kAtKeys + 16 * w;
+    const uint32_t bar = rawfull + (w * kStages + st) * 8, dst = aRaw + (w * kStages + st) * 2048;
+    mbar_expect_tx(bar, 2048);
+    const uint64_t policy = TWO ? policy_evict_last() : policy_evict_first();  // other row tiles read them too, or nobody
+    tma_load_2d(dst, &tmK, bar, kvh * 16, row, policy);
+    tma_load_2d(dst + 1024, &tmV, bar, kvh * 16, row, policy);
+  };
+  if (warp >= 8 && lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(rawfull + ((warp - 8) * kStages + i) * 8, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int j = 0; j < min(kStages, nc); ++j) copy(j);
+  }
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(qfull), kAtConv / 32);
+    mbar_init(qfull, kAtConv);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&kfull[i]), kAtConv / 32);
-      mbar_init(smem_u32(&vfull[i]), kAtConv / 32);
-      mbar_init(smem_u32(&kempty[i]), 1);
-      mbar_init(smem_u32(&vempty[i]), 1);
-      mbar_init(smem_u32(&sfull[i]), 1);
-      mbar_init(smem_u32(&pready[i]), 4);
-      mbar_init(smem_u32(&pvdone[i]), 1);
+      mbar_init(kfull + 8 * i, kAtConv);
+      mbar_init(vfull + 8 * i, kAtConv);
+      mbar_init(kempty + 8 * i, TWO ? streams : 1);
+      mbar_init(vempty + 8 * i, TWO ? streams : 1);
+      mbar_init(sfull + 8 * i, 1);
+      mbar_init(pready + 8 * i, 4);
+      mbar_init(pvdone + 8 * i, 1);
+      mbar_init(drain + 8 * i, 1);
+      mbar_init(turn + 8 * i, 4);
     }
-    mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 16) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == 8) tmem_alloc(smem_u32(tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   auto row_at = [&](int i) {  // of Q and O
-    const int row = r0 + i;
-    return (((size_t)b * n + row / share) * H + kvh * share + row % share) * kAtHd;
+    const int row = r0 + i, q = share == 1 ? row : row / share;
+    return (((size_t)b * n + q) * H + kvh * share + row - q * share) * kAtHd;
   };
-  // steps of stream s, and the chunk of its step i
-  auto steps = [&](int s) { return TWO ? nc : (nc - s + 1) >> 1; };
+  // steps of stream s (the chunk of its step i: i, or 2 i + s)
+  auto steps = [&](int s) { return TWO ? (s < streams ? nc : 0) : (nc - s + 1) >> 1; };
 
-  if (warp >= 8 && warp < 16) {
-    // ---------------- codes to tiles. Lane bits: 0 and 3 the 32 dims, 1, 2 and 4 the row of eight: a store's
-    // 8 lanes cover 4 rows x 2 halves of their 128 bytes, which the swizzle spreads over all banks.
-    const int p = (lane & 1) | ((lane >> 2) & 2), r = (warp - 8) * 8 + ((lane >> 1) & 3) + ((lane >> 4) << 2);
+  if (warp >= 8) {
+    if (kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtOtherRegs));
+    // ---------------- codes to tiles: rows 16 w + 8 u + r of every chunk.
+    // Lane bits 0 and 3: 32 dims; 1, 2 and 4: the row. A store's 8 lanes cover 4 rows x 2 halves of their 128
+    // bytes, which the swizzle spreads over all banks.
+    const int w = warp - 8, p = (lane & 1) | ((lane >> 2) & 2), r = ((lane >> 1) & 3) + ((lane >> 4) << 2);
     const size_t first = (size_t)b * cache.capacity * cache.n_kv + kvh;
     const int gk = 7 - cache.group_log2, gp = (32 * p) >> cache.group_log2;
-    const uint32_t* kc = cache.kc + first * 16 + 4 * p;
-    const uint32_t* vc = cache.vc + first * 16 + 4 * p;
     const uint32_t* ks = cache.ks + (first << gk) + gp;
     const uint32_t* vs = cache.vs + (first << gk) + gp;
-    const uint32_t cstep = (uint32_t)cache.n_kv * 16, sstep = (uint32_t)cache.n_kv << gk;
-    auto load = [&](AtRaw& a, int j) {
+    const uint32_t sstep = (uint32_t)cache.n_kv << gk;
+    struct Scales {  // of the two rows
+      uint32_t k[2], v[2];
+    };
+    auto load = [&](Scales& a, int j) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int key = (c0 + j) * kAtKeys + r + 64 * u;
-        const uint32_t at = (uint32_t)min(key, len - 1);
-        a.k[u] = __ldg(reinterpret_cast<const uint4*>(kc + (uint64_t)at * cstep));
-        a.v[u] = __ldg(reinterpret_cast<const uint4*>(vc + (uint64_t)at * cstep));
-        const uint32_t sk = __ldg(ks + (uint64_t)at * sstep), sv = __ldg(vs + (uint64_t)at * sstep);
-        a.ks[u] = key < len ? sk : 0u;  // past the end: zeros, whatever the codes
-        a.vs[u] = key < len ? sv : 0u;
+        const uint64_t at = (uint64_t)(uint32_t)min((c0 + j) * kAtKeys + 16 * w + 8 * u + r, len - 1) * sstep;
+        a.k[u] = __ldg(ks + at);
+        a.v[u] = __ldg(vs + at);
       }
     };
-    const int box = (p >> 1) * kAtBox, half = (p & 1) * 4;
-    auto expand = [&](uint8_t* dst, const uint4 (&c)[2], const uint32_t (&sc)[2]) {
+    const uint32_t put = (uint32_t)((p >> 1) * kAtBox + (16 * w + r) * 128), half = (p & 1) * 4;
+    auto expand = [&](uint32_t dst, const uint4 (&c)[2], const uint32_t (&sc)[2], int left) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint32_t ss = __byte_perm(sc[u], sc[u], 0x1010), zz = __byte_perm(sc[u], sc[u], 0x3232);
-        const uint32_t w[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
-        uint8_t* row = dst + box + (r + 64 * u) * 128;
+        // past the end: zeros, whatever the codes (decided here: next to its load it would wait for it)
+        const uint32_t y = 16 * w + 8 * u + r < left ? sc[u] : 0u;
+        const uint32_t ss = __byte_perm(y, y, 0x1010), zz = __byte_perm(y, y, 0x3232);
+        const uint32_t word[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int e = 0; e < 4; ++e) {
           uint32_t o[4];
-          kv_word_bf16(w[i], ss, zz, o);
-          *reinterpret_cast<uint4*>(row + (((half + i) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          kv_word_bf16(word[e], ss, zz, o);
+          sts128(dst + put + u * 1024 + (((half + e) ^ r) << 4), o);
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
     };
     bool ok = true;
-    auto chunk = [&](const AtRaw& a, int j) {
-      const int st = j & 1;
+    int landed = 0;  // chunks whose codes have been taken
+    auto chunk = [&](const Scales& a, int j, int raw_st, uint32_t raw_par) {
+      const int st = j & 1, left = len - (c0 + j) * kAtKeys;
       const uint32_t par = (uint32_t)(((j >> 1) - 1) & 1);
-      if (j >= 2) ok = ok && warp_wait(smem_u32(&kempty[st]), par, abort_flag, flag);
+      ok = at_wait(rawfull + (w * kStages + raw_st) * 8, raw_par, abort_flag, flag);
       if (!ok) return;
-      expand(sK + st * kAtTile, a.k, a.ks);
-      if (lane == 0) mbar_arrive(smem_u32(&kfull[st]));
-      if (j >= 2) ok = ok && warp_wait(smem_u32(&vempty[st]), par, abort_flag, flag);
+      uint4 k[2], v[2];
+      const uint32_t src = aRaw + (w * kStages + raw_st) * 2048 + r * 64 + p * 16;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        k[u] = lds128(src + u * 512);
+        v[u] = lds128(src + 1024 + u * 512);
+      }
+      __syncwarp();
+      landed = j + 1;
+      if (lane == 0 && j + kStages < nc) copy(j + kStages);
+      if (j >= 2) ok = at_wait(kempty + 8 * st, par, abort_flag, flag);
       if (!ok) return;
-      expand(sV + st * kAtTile, a.v, a.vs);
-      if (lane == 0) mbar_arrive(smem_u32(&vfull[st]));
+      expand(aK + st * kAtTile, k, a.k, left);
+      if (lane == 0) mbar_arrive(kfull + 8 * st);
+      if (j >= 2) ok = at_wait(vempty + 8 * st, par, abort_flag, flag);
+      if (!ok) return;
+      expand(aV + st * kAtTile, v, a.v, left);
+      if (lane == 0) mbar_arrive(vfull + 8 * st);
     };
-    AtRaw a0, a1;
-    if (nc > 0) load(a0, 0);
-    // Q, zeros past the last row
-    for (int i = threadIdx.x - 256; i < 2 * kAtRows * 16 && nc > 0; i += kAtConv) {
-      const int s = i >> 11, lrow = (i >> 4) & 127, c = i & 15;
-      const int row = TWO ? s * 128 + lrow : (lrow - s * shift) & 127;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (row < rows) x = *reinterpret_cast<const uint4*>(Q + row_at(row) + c * 8);
-      *reinterpret_cast<uint4*>(sQ + s * kAtTile + (c >> 3) * kAtBox + lrow * 128 + (((c & 7) ^ (lrow & 7)) << 4)) = x;
+    Scales sc[kStages];
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i)
+      if (i < nc) load(sc[i], i);
+    // Q, zeros past the last row: 16 lanes a row, eight loads in flight
+    if (nc > 0) {
+#pragma unroll 1
+      for (int i0 = 0; i0 < (TWO ? 2 : 1) * kAtRows; i0 += 8 * 2 * kAtConv) {
+        const int c = lane & 15;
+        uint4 x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int lrow = i0 + (e * kAtConv + w) * 2 + (lane >> 4), row = TWO ? lrow : lrow % kPad;
+          x[e] = row < rows ? *reinterpret_cast<const uint4*>(Q + row_at(row) + c * 8) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int lrow = i0 + (e * kAtConv + w) * 2 + (lane >> 4);
+          const uint32_t v[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+          sts128(aQ + (lrow >> 7) * kAtTile + (c >> 3) * kAtBox + (lrow & 127) * 128 + (((c & 7) ^ (lrow & 7)) << 4), v);
+        }
+      }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(qfull));
-    for (int j = 0; j < nc && ok; j += 2) {
-      if (j + 1 < nc) load(a1, j + 1);
-      chunk(a0, j);
-      if (j + 1 >= nc || !ok) break;
-      if (j + 2 < nc) load(a0, j + 2);
-      chunk(a1, j + 1);
-    }
-  } else if (warp == 16) {
-    if (lane == 0 && nc > 0) {
-      // ---------------- MMA issuer: whichever product can go
-      constexpr uint32_t id_s = idesc_bf16_b(128, 128, 0), id_o = idesc_bf16_b(128, 128, 1);
-      const bool ok = mbar_wait(smem_u32(qfull), 0u, abort_flag, flag);
-      const int total[2] = {steps(0), steps(1)};
-      int si[2] = {0, 0}, pi[2] = {0, 0};  // the stream's next S, its next P V
-      int kused = 0, vused = 0;            // bit s + 2 stage: stream s has issued its product with the stage's chunk
-      uint32_t idle = 0;
-      bool issued = false;
-      while (ok && (pi[0] < total[0] || pi[1] < total[1])) {
-        bool progress = false;
+    if (lane == 0) mbar_arrive(qfull);
+    uint32_t raw_par = 0;
+    for (int j0 = 0; j0 < nc && ok; j0 += kStages, raw_par ^= 1u) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (si[s] < total[s] && si[s] == pi[s]) {
-            const int j = TWO ? si[s] : 2 * si[s] + s, st = j & 1;
-            if ((si[s] == 0 || mbar_test_wait(smem_u32(&pvdone[s]), (uint32_t)((si[s] - 1) & 1))) &&
-                mbar_test_wait(smem_u32(&kfull[st]), (uint32_t)((j >> 1) & 1))) {
-              tc_fence_after();
-              const uint32_t qa = smem_u32(sQ + s * kAtTile), ka = smem_u32(sK + st * kAtTile);
-#pragma unroll
-              for (int kk = 0; kk < kAtHd / 16; ++kk) {
-                const uint32_t off = (uint32_t)((kk >> 2) * kAtBox + (kk & 3) * 32);
-                tc_mma(tmem + (uint32_t)(s * 128), smem_desc_sw128(qa + off), smem_desc_sw128(ka + off), id_s,
-                       kk != 0 ? 1u : 0u);
-              }
-              tc_commit(smem_u32(&sfull[s]));
-              kused |= 1 << (s + 2 * st);
-              if (!TWO || ((kused >> (2 * st)) & 3) == 3) {
-                tc_commit(smem_u32(&kempty[st]));
-                kused &= ~(3 << (2 * st));
-              }
-              ++si[s];
-              issued = true;
-              progress = true;
-            }
-          }
-          if (pi[s] < si[s]) {
-            const int j = TWO ? pi[s] : 2 * pi[s] + s, st = j & 1;
-            if (mbar_test_wait(smem_u32(&pready[s]), (uint32_t)(pi[s] & 1)) &&
-                mbar_test_wait(smem_u32(&vfull[st]), (uint32_t)((j >> 1) & 1))) {
-              tc_fence_after();
-              const uint32_t va = smem_u32(sV + st * kAtTile);
-#pragma unroll
-              for (int kk = 0; kk < kAtKeys / 16; ++kk)
-                tc_mma_ta(tmem + 256u + (uint32_t)(s * 128), tmem + (uint32_t)(s * 128 + kk * 8),
-                          smem_desc_sw128_mn(va + (uint32_t)(kk * 16 * 128), kAtBox), id_o, (pi[s] | kk) != 0 ? 1u : 0u);
-              tc_commit(smem_u32(&pvdone[s]));
-              vused |= 1 << (s + 2 * st);
-              if (!TWO || ((vused >> (2 * st)) & 3) == 3) {
-                tc_commit(smem_u32(&vempty[st]));
-                vused &= ~(3 << (2 * st));
-              }
-              ++pi[s];
-              progress = true;
-            }
-          }
-        }
-        if (progress) {
-          idle = 0;
-        } else if (++idle >= kWaitLimit) {
-          *abort_flag = 1;
-          raise_flag(flag, kFlagTimeout);
-          break;
-        } else if ((idle & 255u) == 255u && *abort_flag) {
-          break;
-        }
+      for (int i = 0; i < kStages; ++i) {
+        const int j = j0 + i;
+        if (j + kStages - 1 < nc) load(sc[(i + kStages - 1) % kStages], j + kStages - 1);
+        if (j < nc && ok) chunk(sc[i], j, i, raw_par);
       }
-      if (issued) {  // nothing in flight when the memory is given back
-        tc_commit(smem_u32(drain));
+    }
+    // a walk that gave up: its copies land before the memory is given back
+    if (!ok && lane == 0)
+      for (int j = landed; j < min(nc, landed + kStages); ++j)
         for (uint32_t it = 0; it < kWaitLimit; ++it)
-          if (mbar_try_wait(smem_u32(drain), 0u)) break;
-      }
-    }
+          if (mbar_try_wait(rawfull + (w * kStages + j % kStages) * 8, (uint32_t)((j / kStages) & 1))) break;
   } else {
-    // ---------------- softmax of stream s: TMEM lane = row
+    if (kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAtSoftRegs));
+    // ---------------- stream s, TMEM lane lrow = copy sub of a row
     const int s = warp >> 2, lrow = (warp & 3) * 32 + lane, ns = steps(s);
-    const int row = TWO ? s * 128 + lrow : (lrow - s * shift) & 127;  // of this CTA
+    const int sub = lrow / kPad, row = TWO ? s * 128 + lrow : lrow % kPad;  // of this CTA
     // a warp without a row only keeps the barriers going
     const bool work = __any_sync(0xffffffffu, row < rows);
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + (uint32_t)(s * 128), tO = tmem + lane_off + 256u + (uint32_t)(s * 128);
+    const bool issuer = (warp & 3) == 0 && lane == 0;
+    bool issued = false;
+    auto issue_s = [&](int i) {  // S of step i, once the products of the step before are done with its P
+      const int j = TWO ? i : 2 * i + s, st = j & 1;
+      if (i == 0 && !mbar_wait(qfull, 0u, abort_flag, flag)) return false;
+      if (i > 0 && !mbar_wait(pvdone + 8 * s, (uint32_t)((i - 1) & 1), abort_flag, flag)) return false;
+      if (!mbar_wait(kfull + 8 * st, (uint32_t)((j >> 1) & 1), abort_flag, flag)) return false;
+      tc_fence_after();
+      const uint32_t qa = aQ + (TWO ? s * kAtTile : 0), ka = aK + st * kAtTile;
+#pragma unroll
+      for (int kk = 0; kk < kAtHd / 16; ++kk) {
+        const uint32_t off = (uint32_t)((kk >> 2) * kAtBox + (kk & 3) * 32);
+        tc_mma(tmem + (uint32_t)(s * 128), smem_desc_sw128(qa + off), smem_desc_sw128(ka + off),
+               idesc_bf16_b(128, 128, 0), kk != 0 ? 1u : 0u);
+      }
+      tc_commit(sfull + 8 * s);
+      tc_commit(kempty + 8 * st);
+      issued = true;
+      return true;
+    };
+    auto issue_pv = [&](int i) {
+      const int j = TWO ? i : 2 * i + s, st = j & 1;
+      if (!mbar_wait(pready + 8 * s, (uint32_t)(i & 1), abort_flag, flag)) return false;
+      if (!mbar_wait(vfull + 8 * st, (uint32_t)((j >> 1) & 1), abort_flag, flag)) return false;
+      tc_fence_after();
+      const uint32_t va = aV + st * kAtTile;
+#pragma unroll
+      for (int kk = 0; kk < kAtKeys / 16; ++kk)
+        tc_mma_ta(tmem + 256u + (uint32_t)(s * 128), tmem + (uint32_t)(s * 128 + kk * 8),
+                  smem_desc_sw128_mn(va + (uint32_t)(kk * 16 * 128), kAtBox), idesc_bf16_b(128, 128, 1),
+                  (i | kk) != 0 ? 1u : 0u);
+      tc_commit(pvdone + 8 * s);
+      tc_commit(vempty + 8 * st);
+      return true;
+    };
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
+    if (issuer && ns > 0) issue_s(0);  // a wait that gives up has set the flag that ends the others
+    __syncwarp();
     for (int i = 0; i < ns; ++i) {
-      ok = warp_wait(smem_u32(&sfull[s]), (uint32_t)(i & 1), abort_flag, flag);
+      ok = at_wait(sfull + 8 * s, (uint32_t)(i & 1), abort_flag, flag);
       if (!ok) break;
       if (work) {
         tc_fence_after();
-        const int left = len - (c0 + (TWO ? i : 2 * i + s)) * kAtKeys;  // keys from the chunk's first on
-        float mx = -INFINITY;
+        float v[kPer];
 #pragma unroll
-        for (int c = 0; c < kAtKeys; c += 32) {
-          float v[32];
-          tmem_ld32(tS + (uint32_t)c, v);
-          tmem_ld_wait();
-          if (left < kAtKeys) {
+        for (int c = 0; c < kPer; c += 32) tmem_ld32(tS + (uint32_t)(sub * kPer + c), *reinterpret_cast<float(*)[32]>(v + c));
+        tmem_ld_wait();
+        // the copy's keys that exist
+        const int left = len - (c0 + (TWO ? i : 2 * i + s)) * kAtKeys - sub * kPer;
+        if (left < kPer) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c + e >= left) v[e] = -INFINITY;
-          }
-          float x4[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-          for (int e = 4; e < 32; ++e) x4[e & 3] = fmaxf(x4[e & 3], v[e]);
-          mx = fmaxf(mx, fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])));
+          for (int e = 0; e < kPer; ++e)
+            if (e >= left) v[e] = -INFINITY;
         }
-        mx *= scale_log2;
+        float x4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int e = 4; e < kPer; e += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            x4[k] = e + 4 + k < kPer ? fmaxf(x4[k], fmaxf(v[e + k], v[e + 4 + k])) : fmaxf(x4[k], v[e + k]);
+        const float mx = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * scale_log2;
         const bool need = mx > m + kApLazy;
         if (__any_sync(0xffffffffu, need)) {
           // the stream's earlier products are in O (its scores were issued after them)
@@ -340,12 +404,12 @@ quant_attention_tc_kernel(const __nv_bfloat16* __restrict__ Q, KvQuant cache, co
           if (i > 0) {
 #pragma unroll 1
             for (int c = 0; c < kAtHd; c += 16) {
-              float v[16];
-              tmem_ld16(tO + (uint32_t)c, v);
+              float u[16];
+              tmem_ld16(tO + (uint32_t)c, u);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] *= f;
-              tmem_st16(tO + (uint32_t)c, v);
+              for (int e = 0; e < 16; ++e) u[e] *= f;
+              tmem_st16(tO + (uint32_t)c, u);
             }
           }
           if (need) {
@@ -353,136 +417,213 @@ quant_attention_tc_kernel(const __nv_bfloat16* __restrict__ Q, KvQuant cache, co
             m = mx;
           }
         }
-        const float sub = m == -INFINITY ? 0.0f : m;
-        float rs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        // the two streams take their exponentials in turn: at once, each would take twice as long, and the tensor
+        // cores would wait for both
+        if (kTurns && streams == 2 && (s == 1 || i > 0)) {
+          ok = at_wait(turn + 8 * s, (uint32_t)((s == 1 ? i : i - 1) & 1), abort_flag, flag);
+          if (!ok) break;
+        }
+        const float sub_m = m == -INFINITY ? 0.0f : -m;
+        const uint64_t sc2 = pack_f2(scale_log2, scale_log2), m2 = pack_f2(sub_m, sub_m);
+        uint64_t rs[2] = {0, 0};
 #pragma unroll
-        for (int c = 0; c < kAtKeys; c += 32) {
-          float v[32];
-          tmem_ld32(tS + (uint32_t)c, v);
-          tmem_ld_wait();
-          if (left < kAtKeys) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c + e >= left) v[e] = -INFINITY;
-          }
+        for (int c = 0; c < kPer; c += 32) {
           float pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float x = ex2_ftz(fmaf(v[e], scale_log2, -sub)), y = ex2_ftz(fmaf(v[e + 1], scale_log2, -sub));
-            rs[(e >> 1) & 3] += x + y;
+            float x, y;
+            unpack_f2(fma_f2(pack_f2(v[c + e], v[c + e + 1]), sc2, m2), x, y);
+            x = ex2_ftz(x);
+            y = ex2_ftz(y);
+            rs[(e >> 1) & 1] = add_f2(rs[(e >> 1) & 1], pack_f2(x, y));
             pk[e >> 1] = __uint_as_float(pack_bf16_tc(x, y));
           }
-          tmem_st16(tS + (uint32_t)(c >> 1), pk);  // P lies over scores that have been read
+          tmem_st16(tS + (uint32_t)((sub * kPer + c) >> 1), pk);  // P lies over scores that have been read
         }
-        l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+        if (NSUB > 1) {  // the other copies' keys
+          float zero[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) zero[e] = 0.0f;
+#pragma unroll
+          for (int c = 0; c < kAtKeys - kPer; c += 32)
+            tmem_st16(tS + (uint32_t)(((sub * kPer + kPer + c) % kAtKeys) >> 1), zero);
+        }
+        if (kTurns && lane == 0) mbar_arrive(turn + 8 * (1 - s));
+        float a0, a1;
+        unpack_f2(add_f2(rs[0], rs[1]), a0, a1);
+        l += a0 + a1;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
       }
-      if (lane == 0) mbar_arrive(smem_u32(&pready[s]));
+      if (kTurns && !work && lane == 0) mbar_arrive(turn + 8 * (1 - s));
+      if (lane == 0) mbar_arrive(pready + 8 * s);
+      if (issuer && issue_pv(i) && i + 1 < ns) issue_s(i + 1);
+      __syncwarp();
     }
-    if (ok && ns > 0) ok = warp_wait(smem_u32(&pvdone[s]), (uint32_t)((ns - 1) & 1), abort_flag, flag);
+    if (issuer && issued) {  // nothing in flight when the memory is given back
+      tc_commit(drain + 8 * s);
+      for (uint32_t it = 0; it < kWaitLimit; ++it)
+        if (mbar_try_wait(drain + 8 * s, 0u)) break;
+    }
+    __syncwarp();
+    if (ok && ns > 0) ok = at_wait(pvdone + 8 * s, (uint32_t)((ns - 1) & 1), abort_flag, flag);
     tc_fence_after();
     const bool have = ok && ns > 0 && work;  // whole warp
-    if (TWO && splits == 1) {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no key: zeros
-      if (work) {
+    const bool direct = TWO && splits == 1;
+    if (!direct) asm volatile("bar.sync 2, 256;" ::: "memory");  // both streams' products are done with the tiles
+    if (work) {
+      const float inv = !direct ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;  // no key: zeros
+      const uint32_t dst = base + (uint32_t)((s * kAtRows + lrow) * kAtLd * 4);
 #pragma unroll
-        for (int c = 0; c < kAtHd; c += 16) {
-          float v[16];
-          if (have) {
-            tmem_ld16(tO + (uint32_t)c, v);
-            tmem_ld_wait();
+      for (int c = 0; c < kAtHd; c += 16) {
+        float u[16];
+        if (have) {
+          tmem_ld16(tO + (uint32_t)c, u);
+          tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] *= inv;
-          } else {
+          for (int e = 0; e < 16; ++e) u[e] *= inv;
+        } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = 0.0f;
-          }
-          if (row < rows) store16_bf16(O + row_at(row) + c, v);
+          for (int e = 0; e < 16; ++e) u[e] = 0.0f;
+        }
+        if (!direct) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) sts_f4(dst + (c + e) * 4, u[e], u[e + 1], u[e + 2], u[e + 3]);
+        } else if (row < rows) {
+          store16_bf16(O + row_at(row) + c, u);
         }
       }
-    } else {
-      asm volatile("bar.sync 2, 256;" ::: "memory");  // both streams' products are done with the tiles
-      float* dst = reinterpret_cast<float*>(smem) + (size_t)(s * kAtRows + (TWO ? lrow : row)) * kAtLd;
-      if (work) {
-#pragma unroll
-        for (int c = 0; c < kAtHd; c += 16) {
-          float v[16];
-          if (have) {
-            tmem_ld16(tO + (uint32_t)c, v);
-            tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = 0.0f;
-          }
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(dst + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-        }
-        s_m[s * kAtRows + (TWO ? lrow : row)] = m;
-        s_l[s * kAtRows + (TWO ? lrow : row)] = l;
-      }
+      s_m[s * kAtRows + lrow] = m;
+      s_l[s * kAtRows + lrow] = l;
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 16) tmem_dealloc(tmem, 512);
-  if (!TWO || splits > 1) {
-    if (splits > 1) cluster_sync_all();
-    // a warp merges a row: source k is CTA k (TWO), or stream k % 2 of CTA k / 2
-    const int src = TWO ? splits : 2 * splits, warps = kAtThreads / 32;
-    for (int i = split * warps + warp; i < rows; i += splits * warps) {
-      const int at = TWO ? i : i + (lane & 1) * kAtRows;  // the row's place in source `lane`
-      const uint32_t cta = TWO ? lane : lane >> 1;
-      const float mk = lane < src ? ld_dsmem_f32(mapa_shared(smem_u32(s_m + at), cta)) : -INFINITY;
-      const float ms = warp_max(mk), sub = ms == -INFINITY ? 0.0f : ms;
-      const float wk = exp2f(mk - sub);
-      const float ls = warp_sum(lane < src ? wk * ld_dsmem_f32(mapa_shared(smem_u32(s_l + at), cta)) : 0.0f);
+  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (!TWO && splits == 1) {
+    // the streams and copies of this CTA alone: eight threads a row
+    for (int i = threadIdx.x; i < rows * 8; i += kAtThreads) {
+      const int r = i >> 3, part = i & 7;
+      float w[2 * NSUB], ms = -INFINITY, ls = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 2 * NSUB; ++k) ms = fmaxf(ms, w[k] = s_m[r + k * kPad]);
+      const float sub = ms == -INFINITY ? 0.0f : ms;
+#pragma unroll
+      for (int k = 0; k < 2 * NSUB; ++k) {
+        w[k] = exp2f(w[k] - sub);
+        ls += w[k] * s_l[r + k * kPad];
+      }
+      const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;  // no key: zeros
+      __nv_bfloat16* dst = O + row_at(r);
+      const float* src = reinterpret_cast<const float*>(smem) + r * kAtLd;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = 4 * (part + 8 * e);
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < 2 * NSUB; ++k) {
+          const float4 x = *reinterpret_cast<const float4*>(src + k * kPad * kAtLd + c);
+          acc.x = fmaf(w[k], x.x, acc.x);
+          acc.y = fmaf(w[k], x.y, acc.y);
+          acc.z = fmaf(w[k], x.z, acc.z);
+          acc.w = fmaf(w[k], x.w, acc.w);
+        }
+        uint2 u;
+        u.x = pack_bf16_tc(acc.x * inv, acc.y * inv);
+        u.y = pack_bf16_tc(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(dst + c) = u;
+      }
+    }
+  } else if (splits > 1) {
+    cluster_sync_all();
+    // a warp merges a row: source k is CTA k (TWO), or stream and copy k % (2 NSUB) of CTA k / (2 NSUB); lane k % 32
+    // holds its weight (at most 64 sources)
+    constexpr int kOf = TWO ? 1 : 2 * NSUB, kStep = TWO ? 0 : kPad;
+    const int src = kOf * splits;
+    for (int i = split * (kAtThreads / 32) + warp; i < rows; i += splits * (kAtThreads / 32)) {
+      float mk[2], wk[2], ms = -INFINITY, ls = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int k = lane + 32 * e;
+        mk[e] = k < src ? ld_dsmem_f32(mapa_shared(smem_u32(s_m + i + k % kOf * kStep), k / kOf)) : -INFINITY;
+        ms = fmaxf(ms, mk[e]);
+      }
+      ms = warp_max(ms);
+      const float sub = ms == -INFINITY ? 0.0f : ms;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int k = lane + 32 * e;
+        wk[e] = exp2f(mk[e] - sub);
+        if (k < src) ls += wk[e] * ld_dsmem_f32(mapa_shared(smem_u32(s_l + i + k % kOf * kStep), k / kOf));
+      }
+      ls = warp_sum(ls);
       const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
 #pragma unroll 4
-      for (int k = 0; k < src; ++k) {
-        const float f = __shfl_sync(0xffffffffu, wk, k);
-        const int place = TWO ? i : i + (k & 1) * kAtRows;
-        const float4 x = ld_dsmem_f4(mapa_shared(
-            smem_u32(reinterpret_cast<float*>(smem) + (size_t)place * kAtLd + 4 * lane), TWO ? k : k >> 1));
-        acc.x = fmaf(f, x.x, acc.x);
-        acc.y = fmaf(f, x.y, acc.y);
-        acc.z = fmaf(f, x.z, acc.z);
-        acc.w = fmaf(f, x.w, acc.w);
-      }
+        for (int k = 32 * e; k < min(src, 32 * e + 32); ++k) {
+          const float f = __shfl_sync(0xffffffffu, wk[e], k & 31);
+          const float4 x = ld_dsmem_f4(
+              mapa_shared(base + (uint32_t)((i + k % kOf * kStep) * kAtLd * 4 + 16 * lane), k / kOf));
+          acc.x = fmaf(f, x.x, acc.x);
+          acc.y = fmaf(f, x.y, acc.y);
+          acc.z = fmaf(f, x.z, acc.z);
+          acc.w = fmaf(f, x.w, acc.w);
+        }
       uint2 u;
       u.x = pack_bf16_tc(acc.x * inv, acc.y * inv);
       u.y = pack_bf16_tc(acc.z * inv, acc.w * inv);
       *reinterpret_cast<uint2*>(O + row_at(i) + 4 * lane) = u;
     }
     __syncwarp();
-    if (splits > 1) cluster_sync_all();  // no CTA leaves while another reads its memory
+    cluster_sync_all();  // no CTA leaves while another reads its memory
   }
 }
 
+using AtKernel = void (*)(const CUtensorMap, const CUtensorMap, const __nv_bfloat16*, KvQuant, const int32_t*, __nv_bfloat16*, int, int, int, int, float, int*);
+
+// Shared-memory opt-in. The register split of the kernels adds up only if they
+// were built with kAtRegs: a launch with fewer would wait for registers for good.
 inline cudaError_t quant_attention_tc_setup() {
-  cudaError_t e =
-      cudaFuncSetAttribute(quant_attention_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAtSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(quant_attention_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAtSmem);
-  return e;
+  const AtKernel all[] = {quant_attention_tc_kernel<true, 1>, quant_attention_tc_kernel<false, 1>,
+                          quant_attention_tc_kernel<false, 2>, quant_attention_tc_kernel<false, 4>};
+  for (int i = 0; i < 4; ++i) {
+    AtKernel k = all[i];
+    cudaFuncAttributes a;
+    cudaError_t e = cudaFuncGetAttributes(&a, k);
+    if (e == cudaSuccess && i < 2 && a.numRegs < kAtRegs) e = cudaErrorInvalidConfiguration;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, at_smem(i == 0));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
-inline cudaError_t quant_attention_tc(const void* Q, const KvQuant& kv, const int32_t* lens, void* O, int B, int n,
-                                      int L, int share, int num_sms, int* flag, cudaStream_t st) {
+// Codes [rows][n_kv * 16] words, boxes of one head's 16 words x 16 rows.
+inline bool at_encode(const TcPlan& pl, CUtensorMap* m, const void* codes, const KvQuant& kv, int B) {
+  const cuuint64_t dim[2] = {(cuuint64_t)kv.n_kv * 16, (cuuint64_t)B * kv.capacity}, stride[1] = {(cuuint64_t)kv.n_kv * 64};
+  const cuuint32_t box[2] = {16, 16}, one[2] = {1, 1};
+  return pl.encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(codes), dim, stride, box, one,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+inline cudaError_t quant_attention_tc(const TcPlan& pl, const void* Q, const KvQuant& kv, const int32_t* lens, void* O, int B, int n,
+                                      int L, int share, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  if (!at_encode(pl, &mk, kv.kc, kv, B) || !at_encode(pl, &mv, kv.vc, kv, B)) return cudaErrorInvalidValue;
   const long long R = (long long)n * share;
-  const bool two = R > 128;
-  const long long tiles = two ? (R + 255) / 256 : 1, units = tiles * B * kv.n_kv;
+  const long long tiles = R > 128 ? (R + 255) / 256 : 1, units = tiles * B * kv.n_kv;
   const int chunks = (L + kAtKeys - 1) / kAtKeys;
   int splits = 1;
-  while (splits < kAtMaxSplits && splits < chunks && units * (splits + 1) <= num_sms) ++splits;
+  while (splits < kAtMaxSplits && splits < chunks && units * (splits + 1) <= pl.num_sms) ++splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * splits), (unsigned)(B * kv.n_kv), 1);
   cfg.blockDim = dim3(kAtThreads, 1, 1);
-  cfg.dynamicSmemBytes = kAtSmem;
+  cfg.dynamicSmemBytes = at_smem(R > 128);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -491,9 +632,12 @@ inline cudaError_t quant_attention_tc(const void* Q, const KvQuant& kv, const in
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, two ? quant_attention_tc_kernel<true> : quant_attention_tc_kernel<false>,
-                            (const __nv_bfloat16*)Q, kv, lens, (__nv_bfloat16*)O, n, L, share, splits,
-                            1.4426950408889634f / sqrtf((float)kAtHd), flag);
+  const AtKernel k = R > 128  ? quant_attention_tc_kernel<true, 1>
+                     : R > 64 ? quant_attention_tc_kernel<false, 1>
+                     : R > 32 ? quant_attention_tc_kernel<false, 2>
+                              : quant_attention_tc_kernel<false, 4>;
+  return cudaLaunchKernelEx(&cfg, k, mk, mv, (const __nv_bfloat16*)Q, kv, lens, (__nv_bfloat16*)O, n, L, share, splits,
+                            1.4426950408889634f / sqrtf((float)kAtHd), pl.flag);
 }
 
 }  // namespace esd

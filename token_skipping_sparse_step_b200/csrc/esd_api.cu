@@ -632,7 +632,7 @@ esd_status k_attention_quant(esd_ctx* c, const void* Q, const esd::KvQuant& kv, 
   if (sizeof(T) == 2 && n <= 16 && n * share <= 16)
     e = esd::quant_attention_rows(Q, kv, lens, O, B, n, L, share, sms, st);
   else if (sizeof(T) == 2)
-    e = esd::quant_attention_tc(Q, kv, lens, O, B, n, L, share, sms, c->flag, st);
+    e = esd::quant_attention_tc(c->tc, Q, kv, lens, O, B, n, L, share, st);
   else
     e = esd::quant_attention_simt<T>(Q, kv, lens, O, B, n, L, share, c->dims.head_dim, sms, st);
   c->launches++;
@@ -1675,7 +1675,8 @@ esd_status esd_partial_attention_quantized(esd_ctx* c, const void* q, const esd_
   esd::KvQuant kv;
   ESD_TRY(check_kv(c, cache, &kv));
   if (L > kv.capacity) return fail(c, ESD_ERR_INVALID_ARG, "length %d above the capacity %d", L, kv.capacity);
-  if ((long long)B * kv.n_kv > 65535) return fail(c, ESD_ERR_UNSUPPORTED, "grid limits");
+  if ((long long)B * kv.n_kv > 65535 || (long long)B * kv.capacity > INT32_MAX)
+    return fail(c, ESD_ERR_UNSUPPORTED, "grid limits");
   cudaStream_t st = (cudaStream_t)stream;
   return c->bf16 ? k_attention_quant<__nv_bfloat16>(c, q, kv, lens, out, B, k, L, st)
                  : k_attention_quant<float>(c, q, kv, lens, out, B, k, L, st);
