@@ -121,15 +121,6 @@ __device__ __forceinline__ void sts_f4(uint32_t addr, float x, float y, float z,
   asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }
 
-// A warp's wait, polled by one lane: 32 lanes that poll take the barrier unit from
-// the warps that arrive.
-__device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* flag) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, flag);
-  __syncwarp();
-  return __all_sync(0xffffffffu, ok);
-}
-
 // Grid (tiles * splits, B * n_kv), cluster (splits). TWO: two row tiles per CTA
 // (NSUB 1); else one of at most 128 / NSUB rows, in NSUB copies.
 template <bool TWO, int NSUB>
@@ -261,34 +252,37 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
       __syncwarp();
     };
     bool ok = true;
-    int landed = 0;  // chunks whose codes have been taken
-    auto chunk = [&](const Scales& a, int j, int raw_st, uint32_t raw_par) {
-      const int st = j & 1, left = len - (c0 + j) * kAtKeys;
-      const uint32_t par = (uint32_t)(((j >> 1) - 1) & 1);
-      ok = at_wait(rawfull + (w * kStages + raw_st) * 8, raw_par, abort_flag, flag);
-      if (!ok) return;
-      uint4 k[2], v[2];
-      const uint32_t src = aRaw + (w * kStages + raw_st) * 2048 + r * 64 + p * 16;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        k[u] = lds128(src + u * 512);
-        v[u] = lds128(src + 1024 + u * 512);
+    int landed = 0;  // chunks whose codes have landed
+    // K of chunk j + 1, then V of chunk j: a V stage that is not free yet does not hold back the next scores
+    auto step = [&](const Scales& ak, const Scales& av, int j) {
+      const uint32_t src = aRaw + w * kStages * 2048 + r * 64 + p * 16;
+      const int jk = j + 1;
+      if (jk < nc) {
+        const int rs = jk % kStages, st = jk & 1;
+        ok = warp_wait(rawfull + (w * kStages + rs) * 8, (uint32_t)((jk / kStages) & 1), abort_flag, flag);
+        if (!ok) return;
+        landed = jk + 1;
+        const uint4 c[2] = {lds128(src + rs * 2048), lds128(src + rs * 2048 + 512)};
+        if (jk >= 2) ok = warp_wait(kempty + 8 * st, (uint32_t)(((jk >> 1) - 1) & 1), abort_flag, flag);
+        if (!ok) return;
+        expand(aK + st * kAtTile, c, ak.k, len - (c0 + jk) * kAtKeys);
+        if (lane == 0) mbar_arrive(kfull + 8 * st);
       }
-      __syncwarp();
-      landed = j + 1;
-      if (lane == 0 && j + kStages < nc) copy(j + kStages);
-      if (j >= 2) ok = at_wait(kempty + 8 * st, par, abort_flag, flag);
-      if (!ok) return;
-      expand(aK + st * kAtTile, k, a.k, left);
-      if (lane == 0) mbar_arrive(kfull + 8 * st);
-      if (j >= 2) ok = at_wait(vempty + 8 * st, par, abort_flag, flag);
-      if (!ok) return;
-      expand(aV + st * kAtTile, v, a.v, left);
-      if (lane == 0) mbar_arrive(vfull + 8 * st);
+      if (j >= 0) {
+        const int rs = j % kStages, st = j & 1;
+        const uint4 c[2] = {lds128(src + rs * 2048 + 1024), lds128(src + rs * 2048 + 1536)};
+        __syncwarp();
+        if (lane == 0 && j + kStages < nc) copy(j + kStages);  // the stage has been read
+        if (j >= 2) ok = warp_wait(vempty + 8 * st, (uint32_t)(((j >> 1) - 1) & 1), abort_flag, flag);
+        if (!ok) return;
+        expand(aV + st * kAtTile, c, av.v, len - (c0 + j) * kAtKeys);
+        if (lane == 0) mbar_arrive(vfull + 8 * st);
+      }
     };
-    Scales sc[kStages];
+    constexpr int kSc = 4;  // chunks of steps and offsets in registers
+    Scales sc[kSc];
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i)
+    for (int i = 0; i < kSc - 1; ++i)
       if (i < nc) load(sc[i], i);
     // Q, zeros past the last row: 16 lanes a row, eight loads in flight
     if (nc > 0) {
@@ -312,13 +306,13 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) mbar_arrive(qfull);
-    uint32_t raw_par = 0;
-    for (int j0 = 0; j0 < nc && ok; j0 += kStages, raw_par ^= 1u) {
+    if (nc > 0) step(sc[0], sc[0], -1);
+    for (int j0 = 0; j0 < nc && ok; j0 += kSc) {
 #pragma unroll
-      for (int i = 0; i < kStages; ++i) {
+      for (int i = 0; i < kSc; ++i) {
         const int j = j0 + i;
-        if (j + kStages - 1 < nc) load(sc[(i + kStages - 1) % kStages], j + kStages - 1);
-        if (j < nc && ok) chunk(sc[i], j, i, raw_par);
+        if (j + kSc - 1 < nc) load(sc[(i + kSc - 1) % kSc], j + kSc - 1);
+        if (j < nc && ok) step(sc[(i + 1) % kSc], sc[i], j);
       }
     }
     // a walk that gave up: its copies land before the memory is given back
@@ -375,7 +369,7 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     if (issuer && ns > 0) issue_s(0);  // a wait that gives up has set the flag that ends the others
     __syncwarp();
     for (int i = 0; i < ns; ++i) {
-      ok = at_wait(sfull + 8 * s, (uint32_t)(i & 1), abort_flag, flag);
+      ok = warp_wait(sfull + 8 * s, (uint32_t)(i & 1), abort_flag, flag);
       if (!ok) break;
       if (work) {
         tc_fence_after();
@@ -420,7 +414,7 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
         // the two streams take their exponentials in turn: at once, each would take twice as long, and the tensor
         // cores would wait for both
         if (kTurns && streams == 2 && (s == 1 || i > 0)) {
-          ok = at_wait(turn + 8 * s, (uint32_t)((s == 1 ? i : i - 1) & 1), abort_flag, flag);
+          ok = warp_wait(turn + 8 * s, (uint32_t)((s == 1 ? i : i - 1) & 1), abort_flag, flag);
           if (!ok) break;
         }
         const float sub_m = m == -INFINITY ? 0.0f : -m;
@@ -467,7 +461,7 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
         if (mbar_try_wait(drain + 8 * s, 0u)) break;
     }
     __syncwarp();
-    if (ok && ns > 0) ok = at_wait(pvdone + 8 * s, (uint32_t)((ns - 1) & 1), abort_flag, flag);
+    if (ok && ns > 0) ok = warp_wait(pvdone + 8 * s, (uint32_t)((ns - 1) & 1), abort_flag, flag);
     tc_fence_after();
     const bool have = ok && ns > 0 && work;  // whole warp
     const bool direct = TWO && splits == 1;
