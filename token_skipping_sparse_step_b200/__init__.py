@@ -141,7 +141,7 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -219,6 +219,8 @@ class Context:
         if st != ESD_OK:
             raise EsdError(st, "esd_create failed")
         self.handle = h
+        # read once: a field of a ctypes structure costs more than the checks that use it
+        self._head_dim, self._d, self._dtype = dims.head_dim, dims.d, _storage_dtype(dims)
 
     # -- plumbing
     def _check(self, st: int):
@@ -334,13 +336,13 @@ class Context:
         self._check(_lib.esd_partial_attention(self.handle, _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                                B, L, k, _ptr(out), _stream(stream)))
 
-    def _check_rows(self, cache, B, what, *tensors):
+    def _check_rows(self, cache, B, what, rows, width, a, b):
         """The tensors of a 4-bit cache call: storage type, contiguous and large enough for the kernels."""
-        if cache.head_dim != self.dims.head_dim or B > cache.batch:
+        if cache.head_dim != self._head_dim or B > cache.batch:
             raise ValueError("the cache has %d sequences of head_dim %d" % (cache.batch, cache.head_dim))
-        dt = self.storage_dtype
-        for t, rows, width in tensors:
-            if t.dtype != dt or not t.is_contiguous() or t.numel() < rows * width or not t.is_cuda:
+        dt, n = self._dtype, rows * width
+        for t in (a, b):
+            if t.dtype != dt or not t.is_contiguous() or t.numel() < n or not t.is_cuda:
                 raise ValueError("%s: contiguous %s CUDA tensors of at least %d x %d" % (what, dt, rows, width))
 
     @staticmethod
@@ -352,7 +354,7 @@ class Context:
         """Write rows k, v [B*n, n_kv_heads * head_dim] at positions idx [B, n]
         (None: 0 .. n - 1) of a 4-bit cache; see esd_kv_quantize."""
         w = cache.n_kv_heads * cache.head_dim
-        self._check_rows(cache, B, "k, v", (k, B * n, w), (v, B * n, w))
+        self._check_rows(cache, B, "k, v", B * n, w, k, v)
         self._check_i32(idx, B * n, "idx")
         self._check(_lib.esd_kv_quantize(self.handle, _ptr(k), _ptr(v), _ptr(idx), B, n, cache._ref, _stream(stream)))
 
@@ -360,7 +362,7 @@ class Context:
         """Read rows at positions idx [B, n] (None: 0 .. n - 1) of a 4-bit cache
         back into k_out, v_out; see esd_kv_dequantize."""
         w = cache.n_kv_heads * cache.head_dim
-        self._check_rows(cache, B, "k_out, v_out", (k_out, B * n, w), (v_out, B * n, w))
+        self._check_rows(cache, B, "k_out, v_out", B * n, w, k_out, v_out)
         self._check_i32(idx, B * n, "idx")
         self._check(_lib.esd_kv_dequantize(self.handle, cache._ref, _ptr(idx), B, n, _ptr(k_out), _ptr(v_out),
                                            _stream(stream)))
@@ -369,8 +371,7 @@ class Context:
         """Attention of q [B*k, d] over the first L rows of a 4-bit cache (of
         sequence b the first lens[b], int32 [B]); see
         esd_partial_attention_quantized."""
-        d = self.dims.d
-        self._check_rows(cache, B, "q, out", (q, B * k, d), (out, B * k, d))
+        self._check_rows(cache, B, "q, out", B * k, self._d, q, out)
         self._check_i32(lens, B, "lens")
         self._check(_lib.esd_partial_attention_quantized(self.handle, _ptr(q), cache._ref, _ptr(lens), B, L, k,
                                                          _ptr(out), _stream(stream)))

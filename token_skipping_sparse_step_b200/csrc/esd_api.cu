@@ -597,16 +597,26 @@ esd_status check_kv_rows(esd_ctx* c, const esd::KvQuant& kv, const int32_t* idx,
   if (((uintptr_t)k | (uintptr_t)v) & 15) return fail(c, ESD_ERR_INVALID_ARG, "rows need 16-byte alignment");
   if (!idx && n > kv.capacity)
     return fail(c, ESD_ERR_INVALID_ARG, "%d rows do not fit the capacity %d", n, kv.capacity);
+  if ((long long)B * n > INT32_MAX || kv.n_kv * (c->dims.head_dim / 8) > 65535)
+    return fail(c, ESD_ERR_UNSUPPORTED, "%d x %d rows of %d heads", B, n, kv.n_kv);
   return ESD_OK;
+}
+
+// Rows per block of the cache kernels: whole rows of about kKvItems items, fewer
+// while that leaves SMs without a block.
+int kv_rows_per_block(const esd_ctx* c, int rows, int per_row) {
+  int rpb = std::max(1, esd::kKvItems / per_row);
+  while (rpb > 1 && (long long)rows < 2LL * c->tc.num_sms * rpb) rpb /= 2;
+  return rpb;
 }
 
 template <typename T>
 esd_status k_kv_quantize(esd_ctx* c, const void* k, const void* v, const int32_t* idx, int B, int n,
                          const esd::KvQuant& kv, cudaStream_t st) {
-  const int per_row = kv.n_kv * (c->dims.head_dim / 16);
-  const long long total = (long long)B * n * per_row;
-  esd::kv_quantize_kernel<T><<<dim3(cdiv(total, 256), 2), 256, 0, st>>>((const T*)k, (const T*)v, idx, total, n,
-                                                                        per_row, kv, c->flag);
+  const int per_row = kv.n_kv * (c->dims.head_dim / 16), rows = B * n, rpb = kv_rows_per_block(c, rows, per_row);
+  const uint32_t magic = (uint32_t)(((1ull << 32) + per_row - 1) / per_row);
+  esd::kv_quantize_kernel<T><<<dim3(cdiv(rows, rpb), 2), esd::kKvThreads, 0, st>>>(
+      (const T*)k, (const T*)v, idx, rows, n, per_row, rpb, magic, kv, c->flag);
   ESD_LAUNCHED(c);
   return ESD_OK;
 }
@@ -614,10 +624,10 @@ esd_status k_kv_quantize(esd_ctx* c, const void* k, const void* v, const int32_t
 template <typename T>
 esd_status k_kv_dequantize(esd_ctx* c, const esd::KvQuant& kv, const int32_t* idx, int B, int n, void* k, void* v,
                            cudaStream_t st) {
-  const int per_row = kv.n_kv * (c->dims.head_dim / 8);
-  const long long total = (long long)B * n * per_row;
-  esd::kv_dequantize_kernel<T><<<dim3(cdiv(total, 256), 2), 256, 0, st>>>(kv, idx, total, n, per_row, (T*)k, (T*)v,
-                                                                          c->flag);
+  const int per_row = kv.n_kv * (c->dims.head_dim / 8), rows = B * n, rpb = kv_rows_per_block(c, rows, per_row);
+  const uint32_t magic = (uint32_t)(((1ull << 32) + per_row - 1) / per_row);
+  esd::kv_dequantize_kernel<T><<<dim3(cdiv(rows, rpb), 2), esd::kKvThreads, 0, st>>>(kv, idx, rows, n, per_row, rpb,
+                                                                                 magic, (T*)k, (T*)v, c->flag);
   ESD_LAUNCHED(c);
   return ESD_OK;
 }

@@ -79,9 +79,9 @@ __device__ __forceinline__ void kv_word_f32(uint32_t w, float s, float z, float 
 __device__ __forceinline__ float pair_step(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float pair_offset(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
 
-// The cache row of row j of sequence b of a call with n rows per sequence: its
-// position is idx[b n + j], or j without idx. -1 for a padding row (negative
-// position), and, with the error flag raised, for a position past the cache.
+// The cache row of row r = b n + j of a call with n rows per sequence: its
+// position is idx[r], or j without idx. -1 for a padding row (negative position),
+// and, with the error flag raised, for a position past the cache.
 __device__ __forceinline__ long long kv_cache_row(const int32_t* __restrict__ idx, int r, int n, int capacity,
                                                   int* flag) {
   const int b = r / n;
@@ -94,114 +94,171 @@ __device__ __forceinline__ long long kv_cache_row(const int32_t* __restrict__ id
   return (long long)b * capacity + pos;
 }
 
+// Both kernels below: a block takes `rpb` whole rows of the call, cut into items
+// (16 values to write, 8 to read back) in the order of memory. Which row an item is
+// in takes one high product: i < 2^16 and per_row <= 2^16 make it exact.
+constexpr int kKvThreads = 256, kKvItems = 2048;  // items of a block, unless a row alone has more
+__device__ __forceinline__ int kv_row_of(int i, uint32_t magic) { return (int)__umulhi((uint32_t)i, magic); }
+
 // ---------------------------------------------------------------------------
 // Rows k, v [B n, n_kv hd] (storage type) into the cache. blockIdx.y: keys or
-// values. A thread takes 16 consecutive values (its eight bytes of codes), so a
-// group is 2, 4 or 8 neighbouring lanes.
+// values. An item is 16 consecutive values (eight bytes of codes), so a group is
+// 2, 4 or 8 neighbouring lanes.
+//
+// Per value the quotient is taken as a product with the reciprocal, rounded by
+// adding 1.5 2^23, and then set right by its exact remainder x - m - c s (c s has 12
+// bits and cancels): more than half a step away, or half a step from an odd code,
+// the neighbour on that side is the nearest. The extremes span the grid, so that
+// only steps near the bottom of the range, whose own rounding is coarse, need the
+// clamp (and a scaling that keeps their reciprocal finite). What bounds it is the
+// instructions, about 11 a value.
 // ---------------------------------------------------------------------------
 template <typename T>
-__global__ void __launch_bounds__(256)
-kv_quantize_kernel(const T* __restrict__ k, const T* __restrict__ v, const int32_t* __restrict__ idx, long long total,
-                   int n, int per_row, KvQuant cache, int* flag) {
-  const long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const bool live = t < total;
-  const long long tc = live ? t : total - 1;  // idle lanes repeat the last one: every lane takes part in the shuffles
-  const int r = (int)(tc / per_row), c = (int)(tc - (long long)r * per_row);
-  const T* src = (blockIdx.y ? v : k) + (size_t)tc * 16;
-  float x[16];
-  {
+__device__ __forceinline__ void kv_load16(const T* p, float (&x)[16], float& lo, float& hi) {
+  if constexpr (sizeof(T) == 2) {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p)), b = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(w);
+    __nv_bfloat162 mn = h[0], mx = h[0];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      mn = __hmin2_nan(mn, h[i]);
+      mx = __hmax2_nan(mx, h[i]);
+    }
+    lo = min_nan(__low2float(mn), __high2float(mn));
+    hi = max_nan(__low2float(mx), __high2float(mx));
+  } else {
     float a[8], b[8];
-    load8_stream(src, a);
-    load8_stream(src + 8, b);
+    load8_stream(p, a);
+    load8_stream(p + 8, b);
+    lo = hi = a[0];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       x[i] = a[i];
       x[8 + i] = b[i];
+      lo = min_nan(lo, min_nan(a[i], b[i]));
+      hi = max_nan(hi, max_nan(a[i], b[i]));
     }
   }
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int i = 1; i < 16; ++i) {
-    lo = min_nan(lo, x[i]);
-    hi = max_nan(hi, x[i]);
-  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kKvThreads)
+kv_quantize_kernel(const T* __restrict__ k, const T* __restrict__ v, const int32_t* __restrict__ idx, int rows, int n,
+                   int per_row, int rpb, uint32_t magic, KvQuant cache, int* flag) {
+  const int r0 = blockIdx.x * rpb, items = min(rpb, rows - r0) * per_row;
+  const T* src = (blockIdx.y ? v : k) + (size_t)r0 * per_row * 16;
+  uint32_t* codes = blockIdx.y ? cache.vc : cache.kc;
+  uint32_t* scales = blockIdx.y ? cache.vs : cache.ks;
   const int lanes = 1 << (cache.group_log2 - 4);
-  for (int o = 1; o < lanes; o <<= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  const float span15 = __fdiv_rn(__fsub_rn(hi, lo), 15.0f);
-  const __nv_bfloat16 zb = __float2bfloat16_rd(fmaf(-16.0f, span15, lo));  // 16 t is exact: one rounding
-  const float z = __bfloat162float(zb);
-  const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, z), 31.0f));
-  const float s = __bfloat162float(sb);
-  // |s| and |z| finite, without a NaN (a NaN among the values is one in lo and hi)
-  const bool fine = fabsf(s) < INFINITY && fabsf(z) < INFINITY;
-  uint32_t pair = 0x7FFF7FFFu;
-  uint32_t words[2] = {0, 0};
-  if (fine) {
-    pair = (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(zb) << 16);
-    if (s > 0.0f) {
-      const float m = fmaf(16.0f, s, z);  // 16 s is exact: one rounding
-      // steps near the bottom of the range are scaled up (exactly) so that their reciprocal is finite
-      const float up = s < 0x1p-60f ? 0x1p64f : 1.0f;
-      const float su = s * up, inv = __frcp_rn(su), half = 0.5f * su;
-      // just below half a step: an odd code gives a tie away, an even one keeps it
+  for (int i0 = 0; i0 < items; i0 += kKvThreads) {
+    const bool live = i0 + (int)threadIdx.x < items;
+    const int i = live ? i0 + (int)threadIdx.x : items - 1;  // idle lanes repeat the last one: every lane takes part in the shuffles
+    const int rr = kv_row_of(i, magic), c = i - rr * per_row;
+    float x[16], lo, hi;
+    kv_load16(src + (size_t)i * 16, x, lo, hi);
+    const long long row = kv_cache_row(idx, r0 + rr, n, cache.capacity, flag);
+    for (int o = 1; o < lanes; o <<= 1) {
+      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    const float span15 = __fdiv_rn(__fsub_rn(hi, lo), 15.0f);
+    const __nv_bfloat16 zb = __float2bfloat16_rd(fmaf(-16.0f, span15, lo));  // 16 t is exact: one rounding
+    const float z = __bfloat162float(zb);
+    const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, z), 31.0f));
+    const float s = __bfloat162float(sb);
+    // |s| and |z| finite, without a NaN (a NaN among the values is one in lo and hi)
+    const bool fine = fabsf(s) < INFINITY && fabsf(z) < INFINITY;
+    const uint32_t pair =
+        fine ? (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(zb) << 16) : 0x7FFF7FFFu;
+    const float m = fmaf(16.0f, s, z);  // 16 s is exact: one rounding
+    uint32_t words[2] = {0, 0};
+    if (fine && s >= 0x1p-60f) {
+      const float inv = __frcp_rn(s);
+      const int half = __float_as_int(0.5f * s);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        float sum[2] = {0.0f, 0.0f};  // the codes of the even and of the odd dims as digits of 4 bits
+#pragma unroll
+        for (int j = 7; j >= 0; --j) {
+          const float d = __fsub_rn(x[8 * w + j], m);
+          const float u = fmaf(d, inv, 12582912.0f);
+          const float cf = u - 12582912.0f;
+          const float rem = fmaf(-cf, s, d);
+          // half a step, or the next number below it where the code is odd (the low bit of u)
+          const float lim = __int_as_float(half - (__float_as_int(u) & 1));
+          const float code = fabsf(rem) > lim ? cf + copysignf(1.0f, rem) : cf;
+          sum[j & 1] = fmaf(sum[j & 1], 16.0f, code);
+        }
+        words[w] = (uint32_t)sum[0] | ((uint32_t)sum[1] << 16);
+      }
+    } else if (fine && s > 0.0f) {
+      const float su = s * 0x1p64f, inv = __frcp_rn(su), half = 0.5f * su;
       const float half_odd = __uint_as_float(__float_as_uint(half) - 1u);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float d = __fsub_rn(x[i], m) * up;
-        // the nearest whole number up to the error of the reciprocal, in the low bits of 1.5 2^23 + c
-        const float u = fmaf(d, inv, 12582912.0f);
-        const float cf = u - 12582912.0f;
+      for (int j = 0; j < 16; ++j) {
+        const float d = __fsub_rn(x[j], m) * 0x1p64f;
+        const float u = fmaf(fminf(fmaxf(d, -su), 16.0f * su), inv, 12582912.0f), cf = u - 12582912.0f;
         int code = __float_as_int(u) - 0x4B400000;
-        // the remainder is exact (c s has 12 bits, and cancels d): it says whether a neighbour is nearer
-        const float rem = fmaf(-cf, su, d);
-        const float lim = (code & 1) ? half_odd : half;
-        code += (rem > lim) - (rem < -lim);
-        code = min(max(code, 0), 15);
-        words[i >> 3] |= (uint32_t)code << kv_shift(i & 7);
+        const float rem = fmaf(-cf, su, d), lim = (code & 1) ? half_odd : half;
+        code = min(max(code + (rem > lim) - (rem < -lim), 0), 15);
+        words[j >> 3] |= (uint32_t)code << kv_shift(j & 7);
       }
     }
-  }
-  if (!live) return;
-  const long long row = kv_cache_row(idx, r, n, cache.capacity, flag);
-  if (row < 0) return;
-  // c: which 16 values of the row
-  uint32_t* codes = (blockIdx.y ? cache.vc : cache.kc) + ((size_t)row * per_row + c) * 2;
-  *reinterpret_cast<uint2*>(codes) = make_uint2(words[0], words[1]);
-  if ((c & (lanes - 1)) == 0) {
-    uint32_t* sc = blockIdx.y ? cache.vs : cache.ks;
-    sc[((size_t)row * per_row + c) >> (cache.group_log2 - 4)] = pair;
+    if (live && row >= 0) {
+      const size_t at = (size_t)row * per_row + c;
+      *reinterpret_cast<uint2*>(codes + at * 2) = make_uint2(words[0], words[1]);
+      if ((c & (lanes - 1)) == 0) scales[at >> (cache.group_log2 - 4)] = pair;
+    }
   }
 }
 
 // ---------------------------------------------------------------------------
 // Rows of the cache back into k_out, v_out [B n, n_kv hd] (storage type); zeros
-// for a padding row. A thread takes one word (8 values).
+// for a padding row. An item is one word (8 values); a thread has four in flight.
+// Bound by the bytes, most of them written.
 // ---------------------------------------------------------------------------
 template <typename T>
-__global__ void __launch_bounds__(256)
-kv_dequantize_kernel(KvQuant cache, const int32_t* __restrict__ idx, long long total, int n, int per_row,
-                     T* __restrict__ k_out, T* __restrict__ v_out, int* flag) {
-  const long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (t >= total) return;
-  const int r = (int)(t / per_row), c = (int)(t - (long long)r * per_row);
-  T* dst = (blockIdx.y ? v_out : k_out) + (size_t)t * 8;
-  const long long row = kv_cache_row(idx, r, n, cache.capacity, flag);
-  uint32_t w = 0, p = 0;  // s = z = 0: zeros
-  if (row >= 0) {
-    w = __ldcs((blockIdx.y ? cache.vc : cache.kc) + (size_t)row * per_row + c);
-    p = __ldg((blockIdx.y ? cache.vs : cache.ks) + (((size_t)row * per_row + c) >> (cache.group_log2 - 3)));
-  }
-  if constexpr (sizeof(T) == 2) {
-    uint32_t o[4];
-    kv_word_bf16(w, __byte_perm(p, p, 0x1010), __byte_perm(p, p, 0x3232), o);
-    *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-  } else {
-    float o[8];
-    kv_word_f32(w, pair_step(p), pair_offset(p), o);
-    Storage<float>::store8(dst, o);
+__global__ void __launch_bounds__(kKvThreads)
+kv_dequantize_kernel(KvQuant cache, const int32_t* __restrict__ idx, int rows, int n, int per_row, int rpb,
+                     uint32_t magic, T* __restrict__ k_out, T* __restrict__ v_out, int* flag) {
+  constexpr int kFly = 4;
+  const int r0 = blockIdx.x * rpb, items = min(rpb, rows - r0) * per_row;
+  T* dst = (blockIdx.y ? v_out : k_out) + (size_t)r0 * per_row * 8;
+  const uint32_t* codes = blockIdx.y ? cache.vc : cache.kc;
+  const uint32_t* scales = blockIdx.y ? cache.vs : cache.ks;
+  for (int i0 = threadIdx.x; i0 < items; i0 += kFly * kKvThreads) {
+    uint32_t w[kFly], p[kFly];
+#pragma unroll
+    for (int e = 0; e < kFly; ++e) {
+      const int i = i0 + e * kKvThreads;
+      w[e] = p[e] = 0;  // s = z = 0: zeros
+      if (i < items) {
+        const int rr = kv_row_of(i, magic);
+        const long long row = kv_cache_row(idx, r0 + rr, n, cache.capacity, flag);
+        if (row >= 0) {
+          const size_t at = (size_t)row * per_row + (i - rr * per_row);
+          w[e] = __ldcs(codes + at);
+          p[e] = __ldg(scales + (at >> (cache.group_log2 - 3)));
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kFly; ++e) {
+      const int i = i0 + e * kKvThreads;
+      if (i >= items) break;
+      if constexpr (sizeof(T) == 2) {
+        uint32_t o[4];
+        kv_word_bf16(w[e], __byte_perm(p[e], p[e], 0x1010), __byte_perm(p[e], p[e], 0x3232), o);
+        __stcs(reinterpret_cast<uint4*>(dst + (size_t)i * 8), make_uint4(o[0], o[1], o[2], o[3]));
+      } else {
+        float o[8];
+        kv_word_f32(w[e], pair_step(p[e]), pair_offset(p[e]), o);
+        Storage<float>::store8(dst + (size_t)i * 8, o);
+      }
+    }
   }
 }
 
