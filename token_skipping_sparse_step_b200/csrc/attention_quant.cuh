@@ -1,4 +1,5 @@
-// Partial attention over the 4-bit key/value cache on the CUDA cores:
+// Partial attention over the 4-bit key/value cache for the float32 models, on the
+// CUDA cores:
 // out = softmax(q K^T / sqrt(hd)) V per head over the first len keys of each
 // sequence, K and V the values that the cache reads back as (kv_quant.cuh), all
 // sums and softmax statistics in float32.
@@ -27,9 +28,9 @@ constexpr int aq_smem_floats(int hd) {
   return (kAqRows + 2 * kAqKeys) * (hd + 4) + kAqRows * (kAqKeys + 4) + 2 * kAqRows;
 }
 
-template <typename T, int HD>
+template <int HD>
 __global__ void __launch_bounds__(256)
-quant_attention_simt_kernel(const T* __restrict__ Q, KvQuant cache, const int32_t* __restrict__ lens, T* __restrict__ O,
+quant_attention_simt_kernel(const float* __restrict__ Q, KvQuant cache, const int32_t* __restrict__ lens, float* __restrict__ O,
                             int n, int L, int share, int splits, float scale_log2) {
   constexpr int LD = HD + 4, LDP = kAqKeys + 4, WPR = HD / 8;
   constexpr int NJ = (HD + 63) / 64;  // dim quads per thread
@@ -51,38 +52,42 @@ quant_attention_simt_kernel(const T* __restrict__ Q, KvQuant cache, const int32_
     const int r = i / (HD / 8), c = (i % (HD / 8)) * 8, row = r0 + r;
     float q[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (row < rows)
-      Storage<T>::load8(Q + (((size_t)b * n + row / share) * H + kvh * share + row % share) * HD + c, q);
+      Storage<float>::load8(Q + (((size_t)b * n + row / share) * H + kvh * share + row % share) * HD + c, q);
     Storage<float>::store8(sQ + r * LD + c, q);
   }
   float o[2][NJ * 4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < NJ * 4; ++i) o[0][i] = o[1][i] = 0.0f;
 
+  // a thread's words of a tile (K, then V) and their steps and offsets, a tile ahead
+  constexpr int kWords = kAqKeys * WPR * 2 / 256;
+  uint32_t cw[kWords], cp[kWords];
+  auto load = [&](int t) {
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+      const int i = tid + j * 256;
+      const bool is_v = i >= kAqKeys * WPR;
+      const int w = is_v ? i - kAqKeys * WPR : i, key = w / WPR, pos = t * kAqKeys + key;
+      const size_t at = (((size_t)b * cache.capacity + min(pos, len - 1)) * cache.n_kv + kvh) * WPR + w % WPR;
+      cw[j] = __ldg((is_v ? cache.vc : cache.kc) + at);
+      cp[j] = __ldg((is_v ? cache.vs : cache.ks) + (at >> (cache.group_log2 - 3)));
+    }
+  };
+  if (t0 < t1) load(t0);
   for (int t = t0; t < t1; ++t) {
     __syncthreads();  // the previous tile is read; Q is written
-    for (int i = tid; i < kAqKeys * WPR * 2; i += 256) {
-      const bool is_v = i >= kAqKeys * WPR;
-      const int w = is_v ? i - kAqKeys * WPR : i;
-      const int key = w / WPR, wd = w % WPR, pos = t * kAqKeys + key;
-      float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (pos < len) {  // keys past the end read as zeros whatever the cache holds there
-        const size_t at = (((size_t)b * cache.capacity + pos) * cache.n_kv + kvh) * WPR + wd;
-        const uint32_t cw = __ldg((is_v ? cache.vc : cache.kc) + at);
-        const uint32_t p = __ldg((is_v ? cache.vs : cache.ks) + (at >> (cache.group_log2 - 3)));
-        if constexpr (sizeof(T) == 2) {
-          uint32_t h[4];
-          kv_word_bf16(cw, __byte_perm(p, p, 0x1010), __byte_perm(p, p, 0x3232), h);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[2 * j] = pair_step(h[j]);
-            x[2 * j + 1] = pair_offset(h[j]);
-          }
-        } else {
-          kv_word_f32(cw, pair_step(p), pair_offset(p), x);
-        }
-      }
+    for (int j = 0; j < kWords; ++j) {
+      const int i = tid + j * 256;
+      const bool is_v = i >= kAqKeys * WPR;
+      const int w = is_v ? i - kAqKeys * WPR : i, key = w / WPR, wd = w % WPR;
+      // keys past the end read as zeros whatever the cache holds there
+      const uint32_t pr = t * kAqKeys + key < len ? cp[j] : 0u;
+      float x[8];
+      kv_word_f32(cw[j], pair_step(pr), pair_offset(pr), x);
       Storage<float>::store8((is_v ? sV : sK) + key * LD + wd * 8, x);
     }
+    if (t + 1 < t1) load(t + 1);
     __syncthreads();
     float s[2][4];
 #pragma unroll
@@ -193,30 +198,28 @@ quant_attention_simt_kernel(const T* __restrict__ Q, KvQuant cache, const int32_
     const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;  // no key: zeros
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] *= inv;
-    Storage<T>::store8(O + (((size_t)b * n + row / share) * H + kvh * share + row % share) * HD + c, acc);
+    Storage<float>::store8(O + (((size_t)b * n + row / share) * H + kvh * share + row % share) * HD + c, acc);
   }
   __syncwarp();
   cluster_sync_all();  // no CTA leaves while another reads its memory
 }
 
 // Shared-memory opt-in of the kernel for head_dim hd.
-template <typename T>
-cudaError_t quant_attention_simt_setup(int hd) {
+inline cudaError_t quant_attention_simt_setup(int hd) {
   const int smem = aq_smem_floats(hd) * (int)sizeof(float);
-  const void* k = hd == 32   ? (const void*)quant_attention_simt_kernel<T, 32>
-                  : hd == 64 ? (const void*)quant_attention_simt_kernel<T, 64>
-                  : hd == 96 ? (const void*)quant_attention_simt_kernel<T, 96>
-                             : (const void*)quant_attention_simt_kernel<T, 128>;
+  const void* k = hd == 32   ? (const void*)quant_attention_simt_kernel<32>
+                  : hd == 64 ? (const void*)quant_attention_simt_kernel<64>
+                  : hd == 96 ? (const void*)quant_attention_simt_kernel<96>
+                             : (const void*)quant_attention_simt_kernel<128>;
   return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
-template <typename T>
-cudaError_t quant_attention_simt(const void* Q, const KvQuant& kv, const int32_t* lens, void* O, int B, int n, int L,
+inline cudaError_t quant_attention_simt(const void* Q, const KvQuant& kv, const int32_t* lens, void* O, int B, int n, int L,
                                  int share, int hd, int num_sms, cudaStream_t st) {
   const long long tiles = ((long long)n * share + kAqRows - 1) / kAqRows, units = tiles * B * kv.n_kv;
   const int key_tiles = (L + kAqKeys - 1) / kAqKeys;
   int splits = 1;
-  while (splits < kAqMaxSplits && splits * 2 <= key_tiles && units * splits * 2 <= 2LL * num_sms) splits *= 2;
+  while (splits < kAqMaxSplits && splits * 2 <= key_tiles && units * splits * 2 <= 3LL * num_sms) splits *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * splits), (unsigned)(B * kv.n_kv), 1);
   cfg.blockDim = dim3(256, 1, 1);
@@ -229,11 +232,11 @@ cudaError_t quant_attention_simt(const void* Q, const KvQuant& kv, const int32_t
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto* k = hd == 32   ? quant_attention_simt_kernel<T, 32>
-            : hd == 64 ? quant_attention_simt_kernel<T, 64>
-            : hd == 96 ? quant_attention_simt_kernel<T, 96>
-                       : quant_attention_simt_kernel<T, 128>;
-  return cudaLaunchKernelEx(&cfg, k, (const T*)Q, kv, lens, (T*)O, n, L, share, splits,
+  auto* k = hd == 32   ? quant_attention_simt_kernel<32>
+            : hd == 64 ? quant_attention_simt_kernel<64>
+            : hd == 96 ? quant_attention_simt_kernel<96>
+                       : quant_attention_simt_kernel<128>;
+  return cudaLaunchKernelEx(&cfg, k, (const float*)Q, kv, lens, (float*)O, n, L, share, splits,
                             1.4426950408889634f / sqrtf((float)hd));
 }
 

@@ -25,8 +25,14 @@
 // through a ring of its own in shared memory; two rows of codes share a 128-byte
 // line whose 16-byte chunks are permuted by the line, so that both access shapes
 // above are free of bank conflicts. Copying through registers instead (a block
-// ahead) took 78 us where this takes less: its addresses and its registers cost
-// the occupancy that hides the latency.
+// ahead) took 78 us where this takes 61 to 66: its addresses and its registers
+// cost the occupancy that hides the latency.
+//
+// What bounds it: 32 sequences x 1536 keys x 32 heads, groups of 64, one row: 66 us,
+// 3.4 TB/s of the 226 MB (a bare copy of those codes in one launch, 64 bytes a row
+// and head, reaches 4.5 TB/s). The bit operations of the expansion (two per pair of
+// values, at half the issue rate) keep their pipe at 57%; shifts taken as products,
+// and a line of blocks cut evenly over all warps of the machine, were no faster.
 //
 // The warps of a CTA take neighbouring heads (the steps and offsets of 2 to 8
 // heads share a 32-byte sector, which they so fetch once) or, when there are too
@@ -34,9 +40,6 @@
 // Every warp leaves (m, l, O) in shared memory, and the CTAs of the cluster merge
 // a share of the outputs each, in (CTA, warp) order.
 #pragma once
-
-#include <algorithm>
-#include <initializer_list>
 
 #include <initializer_list>
 
@@ -362,7 +365,10 @@ template <int NT, int GPH>
 cudaError_t quant_attention_rows_launch(const void* Q, const KvQuant& kv, const int32_t* lens, void* O, int B, int n,
                                         int L, int share, int num_sms, cudaStream_t st) {
   const int units = B * kv.n_kv, blocks = (L + kArKeys - 1) / kArKeys, resident = num_sms * (NT == 1 ? 3 : 2);
-  // the most heads per CTA that still fill the SMs; then slices while they are all resident and none is empty
+  // the most heads per CTA that still fill the SMs (32 x 32 heads x 1536 keys: 66 us with four, 70 with one); then
+  // slices while they are all resident and none is empty (16 heads x 512 keys: 5.7 us in four, 6.5 in one; 16 heads
+  // x 65536 keys: 53 us in sixteen, 95 in four). CTAs of eight warps, for twice the warps in sixteen slices, took
+  // 78 us there: half as many clusters of sixteen are resident at once.
   int wh = 1;
   while (wh < 4 && kv.n_kv % (2 * wh) == 0 && units / (2 * wh) >= num_sms) wh *= 2;
   int splits = 1;

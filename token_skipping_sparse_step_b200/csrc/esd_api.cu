@@ -639,12 +639,17 @@ esd_status k_attention_quant(esd_ctx* c, const void* Q, const esd::KvQuant& kv, 
   ProfScope ps(c, ESD_K_ATTENTION, B * n, st);
   const int sms = c->tc.num_sms;
   cudaError_t e;
-  if (sizeof(T) == 2 && n <= 16 && n * share <= 16)
-    e = esd::quant_attention_rows(Q, kv, lens, O, B, n, L, share, sms, st);
-  else if (sizeof(T) == 2)
-    e = esd::quant_attention_tc(c->tc, Q, kv, lens, O, B, n, L, share, st);
-  else
-    e = esd::quant_attention_simt<T>(Q, kv, lens, O, B, n, L, share, c->dims.head_dim, sms, st);
+  if constexpr (sizeof(T) == 2) {
+    // Up to 16 rows per key/value head on the kernel that expands codes in registers (each tile of 8 rows costs
+    // it a product per code), more on the one that expands them once per 128 keys in shared memory: 32 sequences x
+    // 1536 keys x 32 heads take 66, 74, 79 and 85 us with 1, 8, 9 and 16 rows there, 150 us with 17 here
+    if ((long long)n * share <= 16)
+      e = esd::quant_attention_rows(Q, kv, lens, O, B, n, L, share, sms, st);
+    else
+      e = esd::quant_attention_tc(c->tc, Q, kv, lens, O, B, n, L, share, st);
+  } else {
+    e = esd::quant_attention_simt(Q, kv, lens, O, B, n, L, share, c->dims.head_dim, sms, st);
+  }
   c->launches++;
   if (e != cudaSuccess) return fail(c, ESD_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
   return ESD_OK;
@@ -1425,9 +1430,9 @@ esd_status esd_create(const esd_model_dims* dims, const esd_weights* w, const es
       return ESD_ERR_CUDA;
     }
   }
-  if ((c->bf16 ? esd::quant_attention_simt_setup<__nv_bfloat16>(m.head_dim)
-               : esd::quant_attention_simt_setup<float>(m.head_dim)) != cudaSuccess ||
-      (c->bf16 && (esd::quant_attention_rows_setup() != cudaSuccess || esd::quant_attention_tc_setup() != cudaSuccess)) || cudaDeviceSynchronize() != cudaSuccess) {
+  const cudaError_t qe = !c->bf16 ? esd::quant_attention_simt_setup(m.head_dim) : esd::quant_attention_rows_setup();
+  if (qe != cudaSuccess || (c->bf16 && esd::quant_attention_tc_setup() != cudaSuccess) ||
+      cudaDeviceSynchronize() != cudaSuccess) {
     free_all(c);
     delete c;
     return ESD_ERR_CUDA;
