@@ -338,7 +338,7 @@ def test_used_together_as_a_sparse_step_does(contexts, n):
         assert (kf[at].float() - rows[0].float()).abs().max() < 0.5
 
 
-@pytest.mark.parametrize("n", [1, 24, 150])
+@pytest.mark.parametrize("n", [1, 12, 24, 40, 100, 150])
 def test_captured_and_replayed_and_on_another_stream(contexts, n):
     ctx = contexts(4, 128, "bf16")
     g = torch.Generator(device="cuda").manual_seed(n)
@@ -375,7 +375,7 @@ def test_captured_and_replayed_and_on_another_stream(contexts, n):
     ctx.sync_check()
 
 
-@pytest.mark.parametrize("n", [1, 24, 150])
+@pytest.mark.parametrize("n", [1, 12, 24, 40, 100, 150])
 def test_two_streams_at_once_on_one_context(contexts, n):
     """The calls keep nothing in the context between them: two streams may run them at the same time."""
     ctx = contexts(4, 128, "bf16")
@@ -397,6 +397,20 @@ def test_two_streams_at_once_on_one_context(contexts, n):
     torch.cuda.synchronize()
     for _, _, want, _, outs in sets:
         assert all(torch.equal(o, want) for o in outs)
+
+
+def test_contexts_of_other_head_dims_do_not_disturb_each_other(contexts):
+    """A float32 context whose head_dim the 4-bit cache does not take, made after one of head_dim 128."""
+    first = contexts(2, 128, "f32", max_batch=2, max_len=300)
+    contexts(2, 48, "f32", max_batch=2, max_len=64)
+    cache = _cache(1, 300, 2, 128, 64)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v, q = (torch.randn(300, 256, generator=g, device="cuda") for _ in range(3))
+    first.kv_quantize(k, v, None, 1, 300, cache)
+    o = torch.empty_like(q)
+    first.partial_attention_quantized(q, cache, 1, 300, 300, o)
+    first.sync_check()
+    assert torch.isfinite(o).all()
 
 
 def test_bad_calls_are_refused(contexts):
@@ -421,7 +435,8 @@ def test_bad_calls_are_refused(contexts):
     refused(inv, ctx.partial_attention_quantized, x, cache, 2, 0, 4, o)
     refused(inv, ctx.partial_attention_quantized, x, cache, 2, 64, 0, o)
     refused(inv, ctx.partial_attention_quantized, x, cache, 0, 64, 4, o)
-    for what in ("rows", "type", "dense", "device", "idx", "lens", "batch"):
+    host = esd.KVQuant.empty(2, 64, 4, 128, 64, device="cpu")
+    for what in ("rows", "type", "dense", "device", "idx", "lens", "batch", "host"):
         with pytest.raises(ValueError):
             if what == "rows":
                 ctx.kv_quantize(x[:3], x, None, 2, 2, cache)
@@ -435,6 +450,8 @@ def test_bad_calls_are_refused(contexts):
                 ctx.kv_quantize(x, x, torch.zeros(2, 4, dtype=torch.int64, device="cuda"), 2, 4, cache)
             elif what == "lens":
                 ctx.partial_attention_quantized(x, cache, 2, 64, 4, o, lens=torch.zeros(1, dtype=torch.int32, device="cuda"))
+            elif what == "host":
+                ctx.partial_attention_quantized(x, host, 2, 64, 4, o)
             else:
                 ctx.partial_attention_quantized(x, cache, 3, 64, 4, o)
     # through the C ABI: what the Python holder would not let through

@@ -185,7 +185,7 @@ class KVQuant:
                     raise ValueError("contiguous tensors of one device")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.batch, self.capacity, self.n_kv_heads = k_codes.shape[:3]
-        self.head_dim, self.group = head_dim, head_dim // groups
+        self.head_dim, self.group, self.device = head_dim, head_dim // groups, k_codes.device
         self._view = _KVQuantView(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
                                   self.n_kv_heads, self.capacity, self.group)
         self._ref = ctypes.byref(self._view)
@@ -340,10 +340,13 @@ class Context:
         """The tensors of a 4-bit cache call: storage type, contiguous and large enough for the kernels."""
         if cache.head_dim != self._head_dim or B > cache.batch:
             raise ValueError("the cache has %d sequences of head_dim %d" % (cache.batch, cache.head_dim))
+        if cache.device.type != "cuda":
+            raise ValueError("the cache is not on a CUDA device")
         dt, n = self._dtype, rows * width
         for t in (a, b):
-            if t.dtype != dt or not t.is_contiguous() or t.numel() < n or not t.is_cuda:
-                raise ValueError("%s: contiguous %s CUDA tensors of at least %d x %d" % (what, dt, rows, width))
+            if t.dtype != dt or not t.is_contiguous() or t.numel() < n or t.device != cache.device:
+                raise ValueError("%s: contiguous %s tensors of at least %d x %d on the cache's device"
+                                 % (what, dt, rows, width))
 
     @staticmethod
     def _check_i32(t, n, what):

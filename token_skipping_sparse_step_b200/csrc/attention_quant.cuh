@@ -206,6 +206,7 @@ quant_attention_simt_kernel(const float* __restrict__ Q, KvQuant cache, const in
 
 // Shared-memory opt-in of the kernel for head_dim hd.
 inline cudaError_t quant_attention_simt_setup(int hd) {
+  if (hd % 32) return cudaSuccess;  // refused by the calls; the opt-in of another head_dim's kernel stays as it is
   const int smem = aq_smem_floats(hd) * (int)sizeof(float);
   const void* k = hd == 32   ? (const void*)quant_attention_simt_kernel<32>
                   : hd == 64 ? (const void*)quant_attention_simt_kernel<64>
