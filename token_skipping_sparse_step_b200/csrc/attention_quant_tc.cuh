@@ -20,13 +20,21 @@
 // first warp issues its MMAs too, in the time in which it would wait for them (one
 // thread that issues for both and polls for what can go took 1.4x the time: it
 // stands still while an MMA is queued). 8..15 expand codes, each the same 16 rows of
-// K and of V in every chunk, which it copies itself by TMA through a ring of its own
-// (no other warp waits on it; registers as the ring kept too few bytes in flight:
-// 1.65 us a chunk), the steps and offsets two or three chunks ahead in registers:
-// bf16 tiles [128 keys][64 dims] x 2 in the 128-byte swizzle that TMA would write (K:
+// K and of V in every chunk, the next chunk's K before a V that may have to wait for
+// its stage: they copy codes by TMA through rings of their own (no other warp waits
+// on them; registers as the ring kept too few bytes in flight: 1.65 us a chunk for
+// 1.42), steps and offsets up to three chunks ahead into registers, and write bf16
+// tiles [128 keys][64 dims] x 2 in the 128-byte swizzle that TMA would write (K:
 // K-major operand, V: MN-major); a warp's lanes are laid out so that its 16-byte
 // stores are free of bank conflicts. Without copies the softmax warps take registers
 // from these (setmaxnreg).
+//
+// What bounds it: that chain. 16 x 1024 rows x 4096 keys x 32 heads take 1574 us (700
+// TFLOP/s), 15% less without exponentials, 22% less without products, the same
+// without the expansion; 32 x 64 rows x 6144 keys 1.4 us per 128 keys and CTA, 1.15
+// with every load, expansion and product taken out. A CTA's start and merge cost
+// about 7 us, which shows where each has few chunks (32 x 64 rows x up to 1536 keys:
+// 137 us).
 //
 // The running maximum moves only when a chunk's exceeds it by more than 2^8 (O is
 // then scaled in TMEM; the result O / l is the same). P is rounded to bf16 for its
@@ -130,7 +138,7 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
                           __nv_bfloat16* __restrict__ O, int n, int L, int share, int splits, float scale_log2,
                           int* flag) {
   static_assert(!TWO || NSUB == 1, "copies only of one tile");
-  constexpr bool kTurns = TWO;
+  constexpr bool kTurns = NSUB == 1;
   constexpr bool kSplitRegs = NSUB == 1;
   constexpr int kStages = at_stages(TWO);
   constexpr int kPad = kAtRows / NSUB, kPer = kAtKeys / NSUB;  // lanes of a copy, its keys of a chunk
@@ -580,16 +588,18 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
 
 using AtKernel = void (*)(const CUtensorMap, const CUtensorMap, const __nv_bfloat16*, KvQuant, const int32_t*, __nv_bfloat16*, int, int, int, int, float, int*);
 
-// Shared-memory opt-in. The register split of the kernels adds up only if they
-// were built with kAtRegs: a launch with fewer would wait for registers for good.
-inline cudaError_t quant_attention_tc_setup() {
+// Shared-memory opt-in. The register split of the first two kernels adds up only if
+// they were built with kAtRegs: a launch with fewer would wait for registers for
+// good. Then *usable stays false, and the calls that need them are refused.
+inline cudaError_t quant_attention_tc_setup(bool* usable) {
+  *usable = true;
   const AtKernel all[] = {quant_attention_tc_kernel<true, 1>, quant_attention_tc_kernel<false, 1>,
                           quant_attention_tc_kernel<false, 2>, quant_attention_tc_kernel<false, 4>};
   for (int i = 0; i < 4; ++i) {
     AtKernel k = all[i];
     cudaFuncAttributes a;
     cudaError_t e = cudaFuncGetAttributes(&a, k);
-    if (e == cudaSuccess && i < 2 && a.numRegs < kAtRegs) e = cudaErrorInvalidConfiguration;
+    if (e == cudaSuccess && i < 2 && a.numRegs < kAtRegs) *usable = false;
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, at_smem(i == 0));
     if (e != cudaSuccess) return e;
   }

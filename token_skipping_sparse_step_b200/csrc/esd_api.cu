@@ -61,6 +61,7 @@ struct esd_ctx {
   int device = -1;
   size_t esz = 4;  // bytes per stored element
   bool bf16 = false;
+  bool kv_tc = false;  // the many-row kernels of the 4-bit cache can be launched
 
   const void* embed = nullptr;
   const void* w_out = nullptr;
@@ -643,6 +644,8 @@ esd_status k_attention_quant(esd_ctx* c, const void* Q, const esd::KvQuant& kv, 
     // Up to 16 rows per key/value head on the kernel that expands codes in registers (each tile of 8 rows costs
     // it a product per code), more on the one that expands them once per 128 keys in shared memory: 32 sequences x
     // 1536 keys x 32 heads take 66, 74, 79 and 85 us with 1, 8, 9 and 16 rows there, 150 us with 17 here
+    if ((long long)n * share > 16 && !c->kv_tc)
+      return fail(c, ESD_ERR_UNSUPPORTED, "the library was built with too few registers for %d rows", n * share);
     if ((long long)n * share <= 16)
       e = esd::quant_attention_rows(Q, kv, lens, O, B, n, L, share, sms, st);
     else
@@ -1431,7 +1434,7 @@ esd_status esd_create(const esd_model_dims* dims, const esd_weights* w, const es
     }
   }
   const cudaError_t qe = !c->bf16 ? esd::quant_attention_simt_setup(m.head_dim) : esd::quant_attention_rows_setup();
-  if (qe != cudaSuccess || (c->bf16 && esd::quant_attention_tc_setup() != cudaSuccess) ||
+  if (qe != cudaSuccess || (c->bf16 && esd::quant_attention_tc_setup(&c->kv_tc) != cudaSuccess) ||
       cudaDeviceSynchronize() != cudaSuccess) {
     free_all(c);
     delete c;
