@@ -191,6 +191,20 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     for (int j = 0; j < min(kStages, nc); ++j) copy(j);
   }
+  auto row_at = [&](int i) {  // of Q and O
+    const int row = r0 + i, q = share == 1 ? row : row / share;
+    return (((size_t)b * n + q) * H + kvh * share + row - q * share) * kAtHd;
+  };
+  // the expanding warps' share of Q: 16 lanes a row, eight loads in flight, zeros past the last row
+  auto load_q = [&](uint4 (&x)[8], int i0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int lrow = i0 + (e * kAtConv + warp - 8) * 2 + (lane >> 4), row = TWO ? lrow : lrow % kPad;
+      x[e] = row < rows ? *reinterpret_cast<const uint4*>(Q + row_at(row) + (lane & 15) * 8) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  uint4 xq[8];
+  if (warp >= 8 && nc > 0) load_q(xq, 0);  // lands while the barriers are set up
   if (threadIdx.x == 0) {
     mbar_init(qfull, kAtConv);
     for (int i = 0; i < 2; ++i) {
@@ -207,15 +221,11 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 8) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  auto row_at = [&](int i) {  // of Q and O
-    const int row = r0 + i, q = share == 1 ? row : row / share;
-    return (((size_t)b * n + q) * H + kvh * share + row - q * share) * kAtHd;
-  };
   // steps of stream s (the chunk of its step i: i, or 2 i + s)
   auto steps = [&](int s) { return TWO ? (s < streams ? nc : 0) : (nc - s + 1) >> 1; };
 
@@ -292,21 +302,15 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
 #pragma unroll
     for (int i = 0; i < kSc - 1; ++i)
       if (i < nc) load(sc[i], i);
-    // Q, zeros past the last row: 16 lanes a row, eight loads in flight
     if (nc > 0) {
-#pragma unroll 1
-      for (int i0 = 0; i0 < (TWO ? 2 : 1) * kAtRows; i0 += 8 * 2 * kAtConv) {
-        const int c = lane & 15;
-        uint4 x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int lrow = i0 + (e * kAtConv + w) * 2 + (lane >> 4), row = TWO ? lrow : lrow % kPad;
-          x[e] = row < rows ? *reinterpret_cast<const uint4*>(Q + row_at(row) + c * 8) : make_uint4(0, 0, 0, 0);
-        }
+      for (int i0 = 0; i0 < (TWO ? 2 : 1) * kAtRows; i0 += 8 * 2 * kAtConv) {
+        if (i0 > 0) load_q(xq, i0);
+        const int c = lane & 15;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int lrow = i0 + (e * kAtConv + w) * 2 + (lane >> 4);
-          const uint32_t v[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+          const uint32_t v[4] = {xq[e].x, xq[e].y, xq[e].z, xq[e].w};
           sts128(aQ + (lrow >> 7) * kAtTile + (c >> 3) * kAtBox + (lrow & 127) * 128 + (((c & 7) ^ (lrow & 7)) << 4), v);
         }
       }
@@ -504,7 +508,7 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == 1) tmem_dealloc(tmem, 512);
   if (!TWO && splits == 1) {
     // the streams and copies of this CTA alone: eight threads a row
     for (int i = threadIdx.x; i < rows * 8; i += kAtThreads) {
@@ -622,8 +626,21 @@ inline cudaError_t quant_attention_tc(const TcPlan& pl, const void* Q, const KvQ
   const long long R = (long long)n * share;
   const long long tiles = R > 128 ? (R + 255) / 256 : 1, units = tiles * B * kv.n_kv;
   const int chunks = (L + kAtKeys - 1) / kAtKeys;
+  // Slices of the keys while every CTA has an SM of its own, as many as pay: a step of a stream takes about 3.5 us (two
+  // row tiles; 2.8 us for one, two chunks), a merge of s CTAs about 2 + 1.5 s (32 heads, 192 rows x 768 keys: 26.6,
+  // 22.0, 18.5 and 19.2 us in 1 to 4 slices; 64 rows: 14.4, 15.0, 14.7 and 16.6; 192 rows x 4096 keys: 112, 64, 48
+  // and 39). More CTAs than SMs lose in any case (64 rows x 2048 keys x 96 heads: 28.6 us in one, 41 in two).
   int splits = 1;
-  while (splits < kAtMaxSplits && splits < chunks && units * (splits + 1) <= pl.num_sms) ++splits;
+  float best = 1e30f;
+  for (int k = 1; k <= kAtMaxSplits && k <= chunks && (k == 1 || units * k <= pl.num_sms); ++k) {
+    const int per = (chunks + k - 1) / k;
+    const float t = R > 128 ? 3.5f * per : 2.8f * ((per + 1) / 2);
+    const float all = t + (k > 1 ? 2.0f + 1.5f * k : 0.0f);
+    if (all < best) {
+      best = all;
+      splits = k;
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * splits), (unsigned)(B * kv.n_kv), 1);
   cfg.blockDim = dim3(kAtThreads, 1, 1);
