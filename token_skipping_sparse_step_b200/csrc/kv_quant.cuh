@@ -48,6 +48,26 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// packed pairs of float32
+__device__ __forceinline__ uint64_t pack_f2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack_f2(uint64_t a, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // bits of the code of dim j (0..7) of a word
 __host__ __device__ constexpr int kv_shift(int j) { return 4 * (j >> 1) + 16 * (j & 1); }
 
@@ -178,21 +198,31 @@ kv_quantize_kernel(const T* __restrict__ k, const T* __restrict__ v, const int32
     if (fine && s >= 0x1p-60f) {
       const float inv = __frcp_rn(s);
       const int half = __float_as_int(0.5f * s);
+      const uint64_t m2 = pack_f2(-m, -m), inv2 = pack_f2(inv, inv), s2 = pack_f2(-s, -s), radix = pack_f2(16.0f, 16.0f);
+      const uint64_t round2 = pack_f2(12582912.0f, 12582912.0f), unround2 = pack_f2(-12582912.0f, -12582912.0f);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        float sum[2] = {0.0f, 0.0f};  // the codes of the even and of the odd dims as digits of 4 bits
+        uint64_t sum = 0;  // the codes of the even and of the odd dims as digits of 4 bits
 #pragma unroll
-        for (int j = 7; j >= 0; --j) {
-          const float d = __fsub_rn(x[8 * w + j], m);
-          const float u = fmaf(d, inv, 12582912.0f);
-          const float cf = u - 12582912.0f;
-          const float rem = fmaf(-cf, s, d);
-          // half a step, or the next number below it where the code is odd (the low bit of u)
-          const float lim = __int_as_float(half - (__float_as_int(u) & 1));
-          const float code = fabsf(rem) > lim ? cf + copysignf(1.0f, rem) : cf;
-          sum[j & 1] = fmaf(sum[j & 1], 16.0f, code);
+        for (int j = 6; j >= 0; j -= 2) {
+          const uint64_t d = add_f2(pack_f2(x[8 * w + j], x[8 * w + j + 1]), m2);
+          const uint64_t u = fma_f2(d, inv2, round2), c = add_f2(u, unround2);
+          const uint64_t rem = fma_f2(c, s2, d);
+          float uu[2], cc[2], rr[2];
+          unpack_f2(u, uu[0], uu[1]);
+          unpack_f2(c, cc[0], cc[1]);
+          unpack_f2(rem, rr[0], rr[1]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // half a step, or the next number below it where the code is odd (the low bit of u)
+            const float lim = __int_as_float(half - (__float_as_int(uu[e]) & 1));
+            if (fabsf(rr[e]) > lim) cc[e] += copysignf(1.0f, rr[e]);
+          }
+          sum = fma_f2(sum, radix, pack_f2(cc[0], cc[1]));
         }
-        words[w] = (uint32_t)sum[0] | ((uint32_t)sum[1] << 16);
+        float even, odd;
+        unpack_f2(sum, even, odd);
+        words[w] = (uint32_t)even | ((uint32_t)odd << 16);
       }
     } else if (fine && s > 0.0f) {
       const float su = s * 0x1p64f, inv = __frcp_rn(su), half = 0.5f * su;
