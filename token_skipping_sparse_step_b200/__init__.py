@@ -141,8 +141,13 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _raw_stream(device: int) -> int:
+    """The current stream of a device, without a stream object."""
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _storage_dtype(dims: ModelDims):
@@ -186,6 +191,7 @@ class KVQuant:
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.batch, self.capacity, self.n_kv_heads = k_codes.shape[:3]
         self.head_dim, self.group, self.device = head_dim, head_dim // groups, k_codes.device
+        self._dev, self._width = k_codes.get_device(), self.n_kv_heads * head_dim  # -1: not on a GPU
         self._view = _KVQuantView(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
                                   self.n_kv_heads, self.capacity, self.group)
         self._ref = ctypes.byref(self._view)
@@ -336,48 +342,44 @@ class Context:
         self._check(_lib.esd_partial_attention(self.handle, _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                                B, L, k, _ptr(out), _stream(stream)))
 
-    def _check_rows(self, cache, B, what, rows, width, a, b):
-        """The tensors of a 4-bit cache call: storage type, contiguous and large enough for the kernels."""
-        if cache.head_dim != self._head_dim or B > cache.batch:
-            raise ValueError("the cache has %d sequences of head_dim %d" % (cache.batch, cache.head_dim))
-        if cache.device.type != "cuda":
-            raise ValueError("the cache is not on a CUDA device")
-        dt, n = self._dtype, rows * width
+    def _check_rows(self, cache, B, what, n, a, b, i32):
+        """The tensors of a 4-bit cache call: a and b of the storage type, i32 int32 (or None), contiguous, of at
+        least n and i32[1] elements, on the cache's device."""
+        dev = cache._dev
+        if cache.head_dim != self._head_dim or B > cache.batch or dev < 0:
+            raise ValueError("the cache has %d sequences of head_dim %d on %s" % (cache.batch, cache.head_dim, cache.device))
+        dt = self._dtype
         for t in (a, b):
-            if t.dtype != dt or not t.is_contiguous() or t.numel() < n or t.device != cache.device:
-                raise ValueError("%s: contiguous %s tensors of at least %d x %d on the cache's device"
-                                 % (what, dt, rows, width))
-
-    @staticmethod
-    def _check_i32(t, n, what):
-        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n or not t.is_cuda):
-            raise ValueError("%s: a contiguous int32 CUDA tensor of at least %d" % (what, n))
+            if t.dtype is not dt or t.numel() < n or t.get_device() != dev or not t.is_contiguous():
+                raise ValueError("%s: contiguous %s tensors of at least %d elements on %s" % (what, dt, n, cache.device))
+        t = i32[0]
+        if t is not None and (t.dtype is not torch.int32 or t.numel() < i32[1] or t.get_device() != dev
+                              or not t.is_contiguous()):
+            raise ValueError("positions and lengths: a contiguous int32 tensor of at least %d elements on %s"
+                             % (i32[1], cache.device))
 
     def kv_quantize(self, k, v, idx, B, n, cache: KVQuant, stream=None):
         """Write rows k, v [B*n, n_kv_heads * head_dim] at positions idx [B, n]
         (None: 0 .. n - 1) of a 4-bit cache; see esd_kv_quantize."""
-        w = cache.n_kv_heads * cache.head_dim
-        self._check_rows(cache, B, "k, v", B * n, w, k, v)
-        self._check_i32(idx, B * n, "idx")
-        self._check(_lib.esd_kv_quantize(self.handle, _ptr(k), _ptr(v), _ptr(idx), B, n, cache._ref, _stream(stream)))
+        self._check_rows(cache, B, "k, v", B * n * cache._width, k, v, (idx, B * n))
+        self._check(_lib.esd_kv_quantize(self.handle, k.data_ptr(), v.data_ptr(), _ptr(idx), B, n, cache._ref,
+                                         _raw_stream(cache._dev) if stream is None else _stream(stream)))
 
     def kv_dequantize(self, cache: KVQuant, idx, B, n, k_out, v_out, stream=None):
         """Read rows at positions idx [B, n] (None: 0 .. n - 1) of a 4-bit cache
         back into k_out, v_out; see esd_kv_dequantize."""
-        w = cache.n_kv_heads * cache.head_dim
-        self._check_rows(cache, B, "k_out, v_out", B * n, w, k_out, v_out)
-        self._check_i32(idx, B * n, "idx")
-        self._check(_lib.esd_kv_dequantize(self.handle, cache._ref, _ptr(idx), B, n, _ptr(k_out), _ptr(v_out),
-                                           _stream(stream)))
+        self._check_rows(cache, B, "k_out, v_out", B * n * cache._width, k_out, v_out, (idx, B * n))
+        self._check(_lib.esd_kv_dequantize(self.handle, cache._ref, _ptr(idx), B, n, k_out.data_ptr(), v_out.data_ptr(),
+                                           _raw_stream(cache._dev) if stream is None else _stream(stream)))
 
     def partial_attention_quantized(self, q, cache: KVQuant, B, L, k, out, lens=None, stream=None):
         """Attention of q [B*k, d] over the first L rows of a 4-bit cache (of
         sequence b the first lens[b], int32 [B]); see
         esd_partial_attention_quantized."""
-        self._check_rows(cache, B, "q, out", B * k, self._d, q, out)
-        self._check_i32(lens, B, "lens")
-        self._check(_lib.esd_partial_attention_quantized(self.handle, _ptr(q), cache._ref, _ptr(lens), B, L, k,
-                                                         _ptr(out), _stream(stream)))
+        self._check_rows(cache, B, "q, out", B * k * self._d, q, out, (lens, B))
+        self._check(_lib.esd_partial_attention_quantized(
+            self.handle, q.data_ptr(), cache._ref, _ptr(lens), B, L, k, out.data_ptr(),
+            _raw_stream(cache._dev) if stream is None else _stream(stream)))
 
     def confidence_argmax(self, x_rows, idx, B, L, k, conf_out, tok_out, stream=None):
         self._check(_lib.esd_confidence_argmax(self.handle, _ptr(x_rows), _ptr(idx), B, L, k,
