@@ -29,12 +29,12 @@
 // stores are free of bank conflicts. Without copies the softmax warps take registers
 // from these (setmaxnreg).
 //
-// What bounds it: that chain. 16 x 1024 rows x 4096 keys x 32 heads take 1574 us (700
+// What bounds it: that chain. 16 x 1024 rows x 4096 keys x 32 heads take 1566 us (702
 // TFLOP/s), 15% less without exponentials, 22% less without products, the same
 // without the expansion; 32 x 64 rows x 6144 keys 1.4 us per 128 keys and CTA, 1.15
 // with every load, expansion and product taken out. A CTA's start and merge cost
 // about 7 us, which shows where each has few chunks (32 x 64 rows x up to 1536 keys:
-// 137 us).
+// 135 us).
 //
 // The running maximum moves only when a chunk's exceeds it by more than 2^8 (O is
 // then scaled in TMEM; the result O / l is the same). P is rounded to bf16 for its
@@ -124,6 +124,8 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
   constexpr int kStages = at_stages(TWO);
   constexpr int kPad = kAtRows / NSUB, kPer = kAtKeys / NSUB;  // lanes of a copy, its keys of a chunk
   extern __shared__ __align__(1024) uint8_t smem_at_raw[];
+  grid_launch_dependents();
+  grid_dependency_wait();  // from here on what the kernels before wrote is read
   const uint32_t base = (smem_u32(smem_at_raw) + 1023u) & ~1023u;
   uint8_t* smem = smem_at_raw + (base - smem_u32(smem_at_raw));
   const uint32_t aQ = base;                 // [stream (TWO)][dims 0-63 | 64-127][128 rows]
@@ -152,11 +154,11 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
   const int b = blockIdx.y / cache.n_kv, kvh = blockIdx.y % cache.n_kv;
   const int H = cache.n_kv * share, r0 = tile * 256;
   const int rows = min(n * share - r0, TWO ? 256 : kPad);  // rows of this CTA
+  const int streams = TWO && rows <= kAtRows ? 1 : 2;
+
   const int len = lens ? min(L, max(0, lens[b])) : L;
   const int chunks = (len + kAtKeys - 1) / kAtKeys;
   const int c0 = chunks * split / splits, nc = chunks * (split + 1) / splits - c0;
-
-  const int streams = TWO && rows <= kAtRows ? 1 : 2;
 
   // 16 rows of codes of chunk j into the warp's stage j % kStages
   auto copy = [&](int j) {
@@ -627,13 +629,17 @@ inline cudaError_t quant_attention_tc(const TcPlan& pl, const void* Q, const KvQ
   cfg.blockDim = dim3(kAtThreads, 1, 1);
   cfg.dynamicSmemBytes = at_smem(R > 128);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = splits;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  // started while the kernel before ends only where every CTA is resident at once (192 rows x 768 keys: 20.5 -> 19.2
+  // us a call; 16 x 1024 rows x 4096 keys lose 3%)
+  cfg.numAttrs = units * splits <= pl.num_sms ? 2 : 1;
   const AtKernel k = R > 128  ? quant_attention_tc_kernel<true, 1>
                      : R > 64 ? quant_attention_tc_kernel<false, 1>
                      : R > 32 ? quant_attention_tc_kernel<false, 2>

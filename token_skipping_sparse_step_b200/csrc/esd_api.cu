@@ -616,8 +616,8 @@ esd_status k_kv_quantize(esd_ctx* c, const void* k, const void* v, const int32_t
                          const esd::KvQuant& kv, cudaStream_t st) {
   const int per_row = kv.n_kv * (c->dims.head_dim / 16), rows = B * n, rpb = kv_rows_per_block(c, rows, per_row);
   const uint32_t magic = (uint32_t)(((1ull << 32) + per_row - 1) / per_row);
-  esd::kv_quantize_kernel<T><<<dim3(cdiv(rows, rpb), 2), esd::kKvThreads, 0, st>>>(
-      (const T*)k, (const T*)v, idx, rows, n, per_row, rpb, magic, kv, c->flag);
+  ESD_CUDA(c, launch_pdl(esd::kv_quantize_kernel<T>, dim3(cdiv(rows, rpb), 2), dim3(esd::kKvThreads), st, (const T*)k,
+                         (const T*)v, idx, rows, n, per_row, rpb, magic, kv, c->flag));
   ESD_LAUNCHED(c);
   return ESD_OK;
 }
@@ -627,8 +627,8 @@ esd_status k_kv_dequantize(esd_ctx* c, const esd::KvQuant& kv, const int32_t* id
                            cudaStream_t st) {
   const int per_row = kv.n_kv * (c->dims.head_dim / 8), rows = B * n, rpb = kv_rows_per_block(c, rows, per_row);
   const uint32_t magic = (uint32_t)(((1ull << 32) + per_row - 1) / per_row);
-  esd::kv_dequantize_kernel<T><<<dim3(cdiv(rows, rpb), 2), esd::kKvThreads, 0, st>>>(kv, idx, rows, n, per_row, rpb,
-                                                                                 magic, (T*)k, (T*)v, c->flag);
+  ESD_CUDA(c, launch_pdl(esd::kv_dequantize_kernel<T>, dim3(cdiv(rows, rpb), 2), dim3(esd::kKvThreads), st, kv, idx,
+                         rows, n, per_row, rpb, magic, (T*)k, (T*)v, c->flag));
   ESD_LAUNCHED(c);
   return ESD_OK;
 }
