@@ -1,0 +1,76 @@
+"""Edges of the 4-bit key/value cache on the GPU: groups whose grid float32 cannot
+resolve, scores that are infinite, calls on one stream without a wait between
+them, and the few-row kernel with several heads to a CTA."""
+import numpy as np
+import pytest
+import torch
+
+import kvq_oracle as Q
+import synth
+from helpers import make_context, to_gpu
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def contexts():
+    made = {}
+
+    def get(heads, hd, dtype, max_batch=8, max_len=1024):
+        key = (heads, hd, dtype, max_batch, max_len)
+        if key not in made:
+            dims = synth.ModelDims(n_layers=2, d=heads * hd, n_heads=heads, head_dim=hd, ffn=128, vocab=256, mask_id=255, dtype=dtype)
+            made[key] = make_context(dims, synth.RunConfig(skip_layer=1), max_batch, max_len)[0]
+        return made[key]
+
+    yield get
+    for c in made.values():
+        c.close()
+
+
+def _cache(B, cap, kv, hd, group):
+    import token_skipping_sparse_step_b200 as esd
+    return esd.KVQuant.empty(B, cap, kv, hd, group)
+
+
+def _close_groups(hd, group):
+    """float32 rows of groups that span a few units in the last place (u) just above a number of 8 bits, where
+    16 s + z itself is rounded by several steps: [rows, hd]."""
+    rng = np.random.default_rng(group)
+    rows = []
+    for base in (1.0, -1.0, 1.5, 2.0 ** 20, -(2.0 ** -30), 2.0 ** -55, 3 * 2.0 ** 90):
+        u = 2.0 ** (np.floor(np.log2(abs(base))) - 23)
+        one = lambda k: base + np.asarray(k) * u
+        for k in (*range(0, 36), 63, 64, 255, 4097):
+            rows.append(np.full(hd, one(k)))
+        rows.append(one(1 + np.arange(hd) % 2))                        # 1, 2, 1, 2 units
+        rows.append(one(np.where(np.arange(hd) % group == 5, 32, 23)))  # one value over the top
+        for spread in (2, 3, 9, 40, 200):
+            for _ in range(12):
+                rows.append(one(rng.integers(0, spread, hd) + rng.integers(0, 40)))
+    x = np.stack(rows)
+    return x.astype(np.float32).astype(np.float64)
+
+
+@pytest.mark.parametrize("hd,group", [(32, 32), (64, 64), (128, 32), (128, 128)])
+def test_groups_of_a_few_units_in_the_last_place(contexts, hd, group):
+    """float32 rows whose quotients pass 15 (or fall below 0) are clamped, and do not reach their neighbours' codes."""
+    ctx = contexts(2, hd, "f32", max_batch=1)
+    x = _close_groups(hd, group)
+    rows = len(x)
+    k, v = np.stack([x, x[::-1]], 1), np.stack([x[::-1], x], 1)       # two heads
+    cache = _cache(1, rows, 2, hd, group)
+    out = [torch.empty(rows, 2 * hd, device="cuda") for _ in range(2)]
+    ctx.kv_quantize(to_gpu(k.reshape(rows, -1), torch.float32), to_gpu(v.reshape(rows, -1), torch.float32), None, 1, rows, cache)
+    ctx.kv_dequantize(cache, None, 1, rows, *out)
+    ctx.sync_check()
+    for x, words, scales, back in ((k, cache.k_codes, cache.k_scales, out[0]), (v, cache.v_codes, cache.v_scales, out[1])):
+        c, s, z = Q.quantize(x, group)
+        p = scales[0].float().cpu().numpy().astype(np.float64)
+        assert np.array_equal(p[..., 0], s) and np.array_equal(p[..., 1], z)
+        got = Q.unpack(words[0].cpu().numpy())
+        bad = np.flatnonzero((got != c).any((1, 2)))
+        assert bad.size == 0, "%d of %d rows, the first: %s for %s" % (bad.size, rows, got[bad[0], 0], c[bad[0], 0])
+        assert np.array_equal(back.cpu().numpy().astype(np.float64).reshape(x.shape), Q.values(c, s, z, "f32"))

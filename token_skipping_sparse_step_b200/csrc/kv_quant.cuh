@@ -17,10 +17,13 @@
 // extremes, t = fl(fl(hi - lo) / 15), z = bf16 below fl(lo - 16 t),
 // s = bf16(fl(fl(hi - z) / 31)). z lies at or below lo - 16 t, so the step that
 // takes 31 s + z to hi takes 16 s + z to lo or below: the sixteen values span
-// the group. c is the whole number nearest to (x - m) / s, m = fl(16 s + z), with
-// the difference in float32 and the quotient exact (ties to even), clamped to
-// 0..15. A group of equal values has s = 0 and z their value. A group with a NaN
-// or an infinity, or whose span overflows, reads back as NaN.
+// the group, but for the rounding of s (2^-9 of up to 31 steps, 0.06 s). c is the
+// whole number nearest to (x - m) / s, m = fl(16 s + z), with the difference in
+// float32 and the quotient exact (ties to even), clamped to 0..15: float32 groups of
+// a few units in the last place have steps below the rounding of m, and quotients up
+// to 16. A group of equal values has s = 0 and z their value where that is a bf16
+// number. A group with a NaN or an infinity, or with an offset that bf16 does not
+// hold (a span of 2.4e38 can do), reads back as NaN.
 #pragma once
 
 #include "common.cuh"
@@ -128,9 +131,11 @@ __device__ __forceinline__ int kv_row_of(int i, uint32_t magic) { return (int)__
 // Per value the quotient is taken as a product with the reciprocal, rounded by
 // adding 1.5 2^23, and then set right by its exact remainder x - m - c s (c s has 12
 // bits and cancels): more than half a step away, or half a step from an odd code,
-// the neighbour on that side is the nearest. The extremes span the grid, so that
-// only steps near the bottom of the range, whose own rounding is coarse, need the
-// clamp (and a scaling that keeps their reciprocal finite). What bounds it is the
+// the neighbour on that side is the nearest. Of bf16 values m is exact (their span is
+// at least a unit of their 8 bits, and so is 16 s + z within 24 bits) and the quotients
+// stay within 0..15 by themselves; float32 values need the clamp, and so do steps near
+// the bottom of the range, whose own rounding is coarse (and which are scaled to keep
+// their reciprocal finite). What bounds it is the
 // instructions, about 20 a value at 3.3 of the 4 that an SM can issue: 16 x 4096 rows
 // of 32 heads take 339 us (1.37 GB, 4.0 TB/s). Two values to an instruction where
 // there is one for a pair took 605 to 561 us with the reading back.
@@ -221,6 +226,8 @@ kv_quantize_kernel(const T* __restrict__ k, const T* __restrict__ v, const int32
             // half a step, or the next number below it where the code is odd (the low bit of u)
             const float lim = __int_as_float(half - (__float_as_int(uu[e]) & 1));
             if (fabsf(rr[e]) > lim) cc[e] += copysignf(1.0f, rr[e]);
+            // before it is a digit: a 16 would carry into the next dim's code
+            if constexpr (sizeof(T) == 4) cc[e] = fminf(fmaxf(cc[e], 0.0f), 15.0f);
           }
           sum = fma_f2(sum, radix, pack_f2(cc[0], cc[1]));
         }
