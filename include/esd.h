@@ -369,7 +369,8 @@ esd_status esd_kv_dequantize(esd_ctx* ctx, const esd_kv_quant* cache, const int3
  * sequence b as esd_kv_dequantize reads them back. lens (device int32 [B], may
  * be NULL): sequence b has min(lens[b], L) keys; rows behind them are not
  * attended to, whatever the cache holds there, and the outputs of a sequence
- * without keys are zeros. q, out: [B*k, d] (RoPE already applied to q), 16-byte
+ * without keys are zeros. A row whose scores are all -infinity (an infinite
+ * query) is NaN, as in esd_partial_attention. q, out: [B*k, d] (RoPE already applied to q), 16-byte
  * aligned, not overlapping. Requires B <= max_batch, 1 <= L <= max_len,
  * L <= capacity, 1 <= k <= max_len. */
 esd_status esd_partial_attention_quantized(esd_ctx* ctx, const void* q, const esd_kv_quant* cache,

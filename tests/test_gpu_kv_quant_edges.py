@@ -74,3 +74,51 @@ def test_groups_of_a_few_units_in_the_last_place(contexts, hd, group):
         bad = np.flatnonzero((got != c).any((1, 2)))
         assert bad.size == 0, "%d of %d rows, the first: %s for %s" % (bad.size, rows, got[bad[0], 0], c[bad[0], 0])
         assert np.array_equal(back.cpu().numpy().astype(np.float64).reshape(x.shape), Q.values(c, s, z, "f32"))
+
+
+def _draw(rng, shape, dtype):
+    return Q.store(rng.standard_normal(shape) * np.exp(rng.standard_normal((*shape[:-1], 1))), dtype)
+
+
+def _load(cache, kc, vc):
+    """The oracle's (codes, steps, offsets) [B, L, kv, ...] into the first rows of a cache."""
+    for words, scales, (c, s, z) in ((cache.k_codes, cache.k_scales, kc), (cache.v_codes, cache.v_scales, vc)):
+        L = c.shape[1]
+        words[:, :L] = torch.from_numpy(Q.pack(c).view(np.int32)).cuda()
+        scales[:, :L] = torch.from_numpy(np.stack([s, z], -1)).to(torch.bfloat16).cuda()
+
+
+def _attend(ctx, q, cache, L, lens, dtype):
+    B, n = q.shape[:2]
+    out = torch.full((B * n, q.shape[2] * q.shape[3]), 77.0, dtype=DT[dtype], device="cuda")
+    ctx.partial_attention_quantized(to_gpu(q.reshape(B * n, -1), DT[dtype]), cache, B, L, n, out,
+                                    lens=None if lens is None else to_gpu(np.asarray(lens), torch.int32))
+    ctx.sync_check()
+    return out.float().cpu().numpy().astype(np.float64).reshape(q.shape)
+
+
+@pytest.mark.parametrize("dtype,n", [("bf16", 1), ("bf16", 12), ("bf16", 24), ("bf16", 40), ("bf16", 100), ("bf16", 150),
+                                     ("bf16", 300), ("f32", 3), ("f32", 40)])
+def test_a_row_whose_scores_are_all_minus_infinity_is_nan(contexts, dtype, n):
+    """An infinite query against keys of one sign: the softmax is not defined, and the row must not read as if its
+    sequence had no keys (zeros). The other rows and heads are as ever."""
+    ctx = contexts(4, 128, dtype)
+    rng = np.random.default_rng(n)
+    B, L, lens = 3, 600, [600, 130, 0]
+    k, v = _draw(rng, (B, L, 4, 128), dtype), _draw(rng, (B, L, 4, 128), dtype)
+    k[..., 7] = -np.abs(k[..., 7]) - 16 * np.abs(k).max(-1)     # far below: it reads back negative
+    kc, vc = Q.quantize(Q.store(k, dtype), 64), Q.quantize(v, 64)
+    kk, vv = Q.values(*kc, dtype), Q.values(*vc, dtype)
+    assert (kk[..., 7] < 0).all()
+    q = Q.store(rng.standard_normal((B, n, 4, 128)), dtype)
+    hit = np.zeros((B, n, 4), bool)
+    hit[:, ::3, 1] = hit[:, n - 1, 2] = True
+    q[..., 7] = np.where(hit, np.inf, q[..., 7] / 16)
+    cache = _cache(B, L, 4, 128, 64)
+    _load(cache, kc, vc)
+    got = _attend(ctx, q, cache, L, lens, dtype)
+    want, tol = Q.attention(np.where(hit[..., None], 0.0, q), kk, vv, lens, dtype)
+    assert not got[2].any()                                     # no keys: zeros, whatever the query
+    hit[2] = False
+    assert np.array_equal(np.isnan(got), np.broadcast_to(hit[..., None], got.shape))
+    assert (np.abs(got - want) <= tol)[~hit].all()

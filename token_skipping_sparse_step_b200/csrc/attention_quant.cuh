@@ -195,7 +195,7 @@ quant_attention_simt_kernel(const float* __restrict__ Q, KvQuant cache, const in
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] += w * z[j];
     }
-    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;  // no key: zeros
+    const float inv = len == 0 ? 0.0f : 1.0f / ls;  // no key: zeros (all scores -inf: NaN)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] *= inv;
     Storage<float>::store8(O + (((size_t)b * n + row / share) * H + kvh * share + row % share) * HD + c, acc);

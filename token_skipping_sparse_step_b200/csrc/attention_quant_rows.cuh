@@ -323,7 +323,7 @@ quant_attention_rows_kernel(const __nv_bfloat16* __restrict__ Q, KvQuant cache, 
         ls += wk[e] * ld_dsmem_f32(mapa_shared(smem_u32(&s_l[(k % per_head) * wh + j][row]), k / per_head));
     }
     ls = warp_sum(ls);
-    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;  // no key: zeros
+    const float inv = len == 0 ? 0.0f : 1.0f / ls;  // no key: zeros (all scores -inf: NaN)
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int e = 0; e < 2; ++e)

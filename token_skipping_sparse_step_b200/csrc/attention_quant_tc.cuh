@@ -462,7 +462,7 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     const bool direct = TWO && splits == 1;
     if (!direct) asm volatile("bar.sync 2, 256;" ::: "memory");  // both streams' products are done with the tiles
     if (work) {
-      const float inv = !direct ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;  // no key: zeros
+      const float inv = direct ? 1.0f / l : 1.0f;  // all scores -inf: NaN (no key: zeros below)
       const uint32_t dst = base + (uint32_t)((s * kAtRows + lrow) * kAtLd * 4);
 #pragma unroll
       for (int c = 0; c < kAtHd; c += 16) {
@@ -505,7 +505,7 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
         w[k] = exp2f(w[k] - sub);
         ls += w[k] * s_l[r + k * kPad];
       }
-      const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;  // no key: zeros
+      const float inv = len == 0 ? 0.0f : 1.0f / ls;  // no key: zeros
       __nv_bfloat16* dst = O + row_at(r);
       const float* src = reinterpret_cast<const float*>(smem) + r * kAtLd;
 #pragma unroll
@@ -549,7 +549,7 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
         if (k < src) ls += wk[e] * ld_dsmem_f32(mapa_shared(smem_u32(s_l + i + k % kOf * kStep), k / kOf));
       }
       ls = warp_sum(ls);
-      const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+      const float inv = len == 0 ? 0.0f : 1.0f / ls;
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int e = 0; e < 2; ++e)
