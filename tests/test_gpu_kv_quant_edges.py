@@ -122,3 +122,37 @@ def test_a_row_whose_scores_are_all_minus_infinity_is_nan(contexts, dtype, n):
     hit[2] = False
     assert np.array_equal(np.isnan(got), np.broadcast_to(hit[..., None], got.shape))
     assert (np.abs(got - want) <= tol)[~hit].all()
+
+
+@pytest.mark.parametrize("n", [1, 12, 24, 40, 100, 150])
+def test_calls_that_feed_each_other_without_a_wait_between_them(contexts, n):
+    """Rows written, attended over, the outputs written over the same rows, read back, and attended with: each call may
+    start while the one before it ends. The same calls with a wait after each give the same bits."""
+    ctx = contexts(4, 128, "bf16")
+    g = torch.Generator(device="cuda").manual_seed(n)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+    B, L = 1, 500
+    first, rows = (rnd(L, 512), rnd(L, 512)), [(rnd(n, 512), rnd(n, 512), rnd(n, 512)) for _ in range(8)]
+    idx = torch.arange(0, n, device="cuda", dtype=torch.int32)[None] * (L // n)
+    results = []
+    for wait in (True, False):
+        cache = _cache(B, L, 4, 128, 64)
+        outs = [[torch.empty_like(rows[0][0]) for _ in range(4)] for _ in range(40)]
+        torch.cuda.synchronize()
+        ctx.kv_quantize(*first, None, B, L, cache)
+        for i, (o, p, k, v) in enumerate(outs):
+            a, b, q = rows[i % 8]
+            for call in (lambda: ctx.kv_quantize(a, b, idx, B, n, cache),
+                         lambda: ctx.partial_attention_quantized(q, cache, B, L, n, o),
+                         lambda: ctx.kv_quantize(o, q, idx, B, n, cache),
+                         lambda: ctx.kv_dequantize(cache, idx, B, n, k, v),
+                         lambda: ctx.partial_attention_quantized(v, cache, B, L, n, p)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+        ctx.sync_check()
+        results.append((outs, cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales))
+    for one, two in zip(results[0][0], results[1][0]):
+        assert all(torch.equal(x, y) for x, y in zip(one, two))
+    assert all(torch.equal(x, y) for x, y in zip(results[0][1:], results[1][1:]))
+    assert not torch.equal(results[0][0][0][0], results[0][0][1][0])    # the rows that were written are attended over

@@ -80,7 +80,7 @@ constexpr int ar_smem() {
 // cluster (splits, 1, 1); wh: heads per CTA (1, 2 or 4).
 template <int NT, int GPH>
 __global__ void __launch_bounds__(kArWarps * 32, NT == 1 ? 4 : 2)
-quant_attention_rows_kernel(const __nv_bfloat16* __restrict__ Q, KvQuant cache, const int32_t* __restrict__ lens,
+quant_attention_rows_kernel(const __nv_bfloat16* Q, KvQuant cache, const int32_t* lens,
                             __nv_bfloat16* __restrict__ O, int n, int L, int share, int splits, int wh,
                             float scale_log2) {
   constexpr int kRows = 8 * NT, kStage = ar_stage<GPH>(), kGlog = GPH == 4 ? 5 : GPH == 2 ? 6 : 7;

@@ -115,7 +115,7 @@ __device__ __forceinline__ void sts_f4(uint32_t addr, float x, float y, float z,
 template <bool TWO, int NSUB>
 __global__ void __launch_bounds__(kAtThreads, 1)
 quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                          const __nv_bfloat16* __restrict__ Q, KvQuant cache, const int32_t* __restrict__ lens,
+                          const __nv_bfloat16* Q, KvQuant cache, const int32_t* lens,
                           __nv_bfloat16* __restrict__ O, int n, int L, int share, int splits, float scale_log2,
                           int* flag) {
   static_assert(!TWO || NSUB == 1, "copies only of one tile");
@@ -230,8 +230,8 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const uint64_t at = (uint64_t)(uint32_t)min((c0 + j) * kAtKeys + 16 * w + 8 * u + r, len - 1) * sstep;
-        a.k[u] = __ldg(ks + at);
-        a.v[u] = __ldg(vs + at);
+        a.k[u] = ks[at];
+        a.v[u] = vs[at];
       }
     };
     const uint32_t put = (uint32_t)((p >> 1) * kAtBox + (16 * w + r) * 128), half = (p & 1) * 4;

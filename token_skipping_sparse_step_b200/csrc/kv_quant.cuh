@@ -105,7 +105,7 @@ __device__ __forceinline__ float pair_offset(uint32_t p) { return __uint_as_floa
 // The cache row of row r = b n + j of a call with n rows per sequence: its
 // position is idx[r], or j without idx. -1 for a padding row (negative position),
 // and, with the error flag raised, for a position past the cache.
-__device__ __forceinline__ long long kv_cache_row(const int32_t* __restrict__ idx, int r, int n, int capacity,
+__device__ __forceinline__ long long kv_cache_row(const int32_t* idx, int r, int n, int capacity,
                                                   int* flag) {
   const int b = r / n;
   const int pos = idx ? idx[r] : r - b * n;
@@ -120,6 +120,13 @@ __device__ __forceinline__ long long kv_cache_row(const int32_t* __restrict__ id
 // Both kernels below: a block takes `rpb` whole rows of the call, cut into items
 // (16 values to write, 8 to read back) in the order of memory. Which row an item is
 // in takes one high product: i < 2^16 and per_row <= 2^16 make it exact.
+//
+// These kernels and the attention kernels over the cache may start before the kernel
+// ahead of them ends, which may be the one that writes what they read. They wait for
+// it, and read by plain loads (or asynchronous copies) alone: the read-only path
+// (__ldg, or const __restrict__ parameters) is for data that nobody writes while the
+// kernel lives. It costs nothing but 1% of the shortest (192 rows x 768 keys attended
+// over: 18.5 -> 18.7 us).
 constexpr int kKvThreads = 256, kKvItems = 2048;  // items of a block, unless a row alone has more
 __device__ __forceinline__ int kv_row_of(int i, uint32_t magic) { return (int)__umulhi((uint32_t)i, magic); }
 
@@ -173,7 +180,7 @@ __device__ __forceinline__ void kv_load16(const T* p, float (&x)[16], float& lo,
 
 template <typename T>
 __global__ void __launch_bounds__(kKvThreads)
-kv_quantize_kernel(const T* __restrict__ k, const T* __restrict__ v, const int32_t* __restrict__ idx, int rows, int n,
+kv_quantize_kernel(const T* k, const T* v, const int32_t* idx, int rows, int n,
                    int per_row, int rpb, uint32_t magic, KvQuant cache, int* flag) {
   grid_launch_dependents();
   grid_dependency_wait();
@@ -264,7 +271,7 @@ kv_quantize_kernel(const T* __restrict__ k, const T* __restrict__ v, const int32
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(kKvThreads)
-kv_dequantize_kernel(KvQuant cache, const int32_t* __restrict__ idx, int rows, int n, int per_row, int rpb,
+kv_dequantize_kernel(KvQuant cache, const int32_t* idx, int rows, int n, int per_row, int rpb,
                      uint32_t magic, T* __restrict__ k_out, T* __restrict__ v_out, int* flag) {
   grid_launch_dependents();
   grid_dependency_wait();
@@ -285,7 +292,7 @@ kv_dequantize_kernel(KvQuant cache, const int32_t* __restrict__ idx, int rows, i
         if (row >= 0) {
           const size_t at = (size_t)row * per_row + (i - rr * per_row);
           w[e] = __ldcs(codes + at);
-          p[e] = __ldg(scales + (at >> (cache.group_log2 - 3)));
+          p[e] = scales[at >> (cache.group_log2 - 3)];
         }
       }
     }
