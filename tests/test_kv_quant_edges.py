@@ -2,6 +2,9 @@
 needed for."""
 import os
 import re
+import subprocess
+
+import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "token_skipping_sparse_step_b200", "csrc")
@@ -25,3 +28,65 @@ def test_kernels_that_start_early_do_not_read_by_the_read_only_path():
         assert not re.search(r"__ldg\s*\(|\.global\.nc\b", code), name
         assert not re.search(r"\bconst\s+\w+\s*\*\s*__restrict__", code), name
     assert waiting == ["attention_quant_rows.cuh", "attention_quant_tc.cuh", "kv_quant.cuh"]
+
+
+WALK = r"""
+#include "copy_window.h"
+#include <cstdio>
+#include <cstdlib>
+#include <set>
+#include <algorithm>
+// The walk of the expanding warps: K of chunk j + 1 is waited for, its stage may not come free, then V of chunk j is
+// read, which frees the chunk's ring stage for the copy of chunk j + stages, and its stage may not come free. It gives
+// up at its wait number `at`. Prints what is in flight then, and what is drained.
+int main(int argc, char** argv) {
+  const int nc = atoi(argv[1]), stages = atoi(argv[2]), at = atoi(argv[3]);
+  esd::CopyWindow w;
+  std::set<int> flying;
+  auto copy = [&](int j) { w.start(j); flying.insert(j); };
+  int waits = 0;
+  auto wait = [&] { return waits++ != at; };
+  for (int j = 0; j < std::min(stages, nc); ++j) copy(j);
+  bool ok = true;
+  for (int j = -1; j < nc && ok; ++j) {
+    if (j + 1 < nc) {
+      if (!(ok = wait())) break;
+      w.land(j + 1);
+      flying.erase(j + 1);
+      if (j + 1 >= 2 && !(ok = wait())) break;
+    }
+    if (j >= 0) {
+      if (j + stages < nc) copy(j + stages);
+      if (j >= 2 && !(ok = wait())) break;
+    }
+  }
+  printf("%d\n", (int)ok);
+  for (int j : flying) printf("%d ", j);
+  printf("\n");
+  w.drain([](int j) { printf("%d ", j); });
+  printf("\n");
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def walk(tmp_path_factory):
+    d = tmp_path_factory.mktemp("walk")
+    (d / "walk.cpp").write_text(WALK)
+    subprocess.run(["g++", "-std=c++17", "-I", CSRC, str(d / "walk.cpp"), "-o", str(d / "walk")], check=True)
+    return str(d / "walk")
+
+
+@pytest.mark.parametrize("stages", [2, 3])
+@pytest.mark.parametrize("nc", [1, 2, 3, 7])
+def test_a_walk_that_gives_up_waits_for_the_copies_in_flight_and_no_others(walk, nc, stages):
+    gave_up = 0
+    for at in range(3 * nc + 2):
+        ok, flying, drained = subprocess.run([walk, str(nc), str(stages), str(at)], capture_output=True, text=True,
+                                             check=True).stdout.split("\n")[:3]
+        assert flying == drained, (nc, stages, at)
+        gave_up += ok == "0"
+    assert gave_up >= nc
+    # the kernel keeps its copies in the same window
+    code = _code("attention_quant_tc.cuh")
+    assert "copies.start(j)" in code and "copies.land(jk)" in code and "copies.drain(" in code and "landed" not in code

@@ -41,7 +41,7 @@ def _nvcc() -> str:
 
 def sources():
     return [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC))
-            if f.endswith((".cu", ".cuh")) and f != "stream_probe.cu"]
+            if f.endswith((".cu", ".cuh", ".h")) and f != "stream_probe.cu"]
 
 
 def needs_build() -> bool:

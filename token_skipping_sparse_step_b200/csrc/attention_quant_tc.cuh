@@ -45,6 +45,7 @@
 #pragma once
 
 #include "attention_pair.cuh"
+#include "copy_window.h"
 #include "kv_quant.cuh"
 
 namespace esd {
@@ -161,7 +162,9 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
   const int c0 = chunks * split / splits, nc = chunks * (split + 1) / splits - c0;
 
   // 16 rows of codes of chunk j into the warp's stage j % kStages
+  CopyWindow copies;  // started: lane 0's
   auto copy = [&](int j) {
+    copies.start(j);
     const int w = warp - 8, st = j % kStages, row = b * cache.capacity + (c0 + j) * kAtKeys + 16 * w;
     const uint32_t bar = rawfull + (w * kStages + st) * 8, dst = aRaw + (w * kStages + st) * 2048;
     mbar_expect_tx(bar, 2048);
@@ -253,7 +256,6 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
       __syncwarp();
     };
     bool ok = true;
-    int landed = 0;  // chunks whose codes have landed
     // K of chunk j + 1, then V of chunk j: a V stage that is not free yet does not hold back the next scores
     auto step = [&](const Scales& ak, const Scales& av, int j) {
       const uint32_t src = aRaw + w * kStages * 2048 + r * 64 + p * 16;
@@ -262,7 +264,7 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
         const int rs = jk % kStages, st = jk & 1;
         ok = warp_wait(rawfull + (w * kStages + rs) * 8, (uint32_t)((jk / kStages) & 1), abort_flag, flag);
         if (!ok) return;
-        landed = jk + 1;
+        copies.land(jk);
         const uint4 c[2] = {lds128(src + rs * 2048), lds128(src + rs * 2048 + 512)};
         if (jk >= 2) ok = warp_wait(kempty + 8 * st, (uint32_t)(((jk >> 1) - 1) & 1), abort_flag, flag);
         if (!ok) return;
@@ -312,9 +314,10 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
     }
     // a walk that gave up: its copies land before the memory is given back
     if (!ok && lane == 0)
-      for (int j = landed; j < min(nc, landed + kStages); ++j)
+      copies.drain([&](int j) {
         for (uint32_t it = 0; it < kWaitLimit; ++it)
           if (mbar_try_wait(rawfull + (w * kStages + j % kStages) * 8, (uint32_t)((j / kStages) & 1))) break;
+      });
   } else {
     if (kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAtSoftRegs));
     // ---------------- stream s, TMEM lane lrow = copy sub of a row
