@@ -318,7 +318,8 @@ esd_status esd_partial_attention(esd_ctx* ctx, const void* q, const void* k_cach
 
 /* Key/value cache in 4 bits (no counterpart in the papers: it holds the K and V
  * of the partial cache in about a quarter of the bytes, for long contexts and
- * large batches). Memory owned by the caller, 16-byte aligned:
+ * large batches). Memory of the context's device, owned by the caller, 16-byte
+ * aligned:
  *  k_codes, v_codes   uint32 [B, capacity, n_kv_heads, head_dim / 8]: 4-bit
  *    codes, dim 2i of a word's eight in bits 4i..4i+3, dim 2i+1 in bits
  *    16+4i..16+4i+3;

@@ -5,6 +5,7 @@ import re
 import subprocess
 
 import pytest
+import torch
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "token_skipping_sparse_step_b200", "csrc")
@@ -90,3 +91,36 @@ def test_a_walk_that_gives_up_waits_for_the_copies_in_flight_and_no_others(walk,
     # the kernel keeps its copies in the same window
     code = _code("attention_quant_tc.cuh")
     assert "copies.start(j)" in code and "copies.land(jk)" in code and "copies.drain(" in code and "landed" not in code
+
+
+class _Rows:
+    """A tensor of a device that is not here, as far as the checks look."""
+    dtype = torch.bfloat16
+
+    def __init__(self, device):
+        self.device = device
+
+    def numel(self):
+        return 1 << 20
+
+    def get_device(self):
+        return self.device
+
+    def is_contiguous(self):
+        return True
+
+
+@pytest.mark.parametrize("device", [0, 1])
+def test_a_cache_on_another_device_than_the_context_is_refused(device):
+    """Its kernels would follow the other device's addresses, on that device's stream."""
+    import token_skipping_sparse_step_b200 as esd
+    ctx = object.__new__(esd.Context)
+    ctx._head_dim, ctx._d, ctx._dtype, ctx._dev = 128, 512, torch.bfloat16, 0
+    cache = esd.KVQuant.empty(2, 8, 4, 128, device="cpu")
+    cache._dev = device
+    rows = _Rows(device)
+    if device == 0:
+        ctx._check_rows(cache, 2, "k, v", 100, rows, rows, (None, 8))
+    else:
+        with pytest.raises(ValueError, match="context"):
+            ctx._check_rows(cache, 2, "k, v", 100, rows, rows, (None, 8))

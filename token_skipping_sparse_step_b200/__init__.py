@@ -227,6 +227,7 @@ class Context:
         self.handle = h
         # read once: a field of a ctypes structure costs more than the checks that use it
         self._head_dim, self._d, self._dtype = dims.head_dim, dims.d, _storage_dtype(dims)
+        self._dev = torch.cuda.current_device()  # the context's device: the one that was current
 
     # -- plumbing
     def _check(self, st: int):
@@ -344,10 +345,11 @@ class Context:
 
     def _check_rows(self, cache, B, what, n, a, b, i32):
         """The tensors of a 4-bit cache call: a and b of the storage type, i32 int32 (or None), contiguous, of at
-        least n and i32[1] elements, on the cache's device."""
+        least n and i32[1] elements, on the device of the context and the cache."""
         dev = cache._dev
-        if cache.head_dim != self._head_dim or B > cache.batch or dev < 0:
-            raise ValueError("the cache has %d sequences of head_dim %d on %s" % (cache.batch, cache.head_dim, cache.device))
+        if cache.head_dim != self._head_dim or B > cache.batch or dev != self._dev:
+            raise ValueError("the cache has %d sequences of head_dim %d on %s (the context: head_dim %d on cuda:%d)"
+                             % (cache.batch, cache.head_dim, cache.device, self._head_dim, self._dev))
         dt = self._dtype
         for t in (a, b):
             if t.dtype is not dt or t.numel() < n or t.get_device() != dev or not t.is_contiguous():
