@@ -156,3 +156,65 @@ def test_calls_that_feed_each_other_without_a_wait_between_them(contexts, n):
         assert all(torch.equal(x, y) for x, y in zip(one, two))
     assert all(torch.equal(x, y) for x, y in zip(results[0][1:], results[1][1:]))
     assert not torch.equal(results[0][0][0][0], results[0][0][1][0])    # the rows that were written are attended over
+
+
+@pytest.mark.parametrize("B,heads,kv,n,group", [(40, 8, 8, 1, 64), (40, 16, 8, 6, 32), (40, 8, 8, 9, 128),      # 2 heads to a CTA
+                                                (80, 8, 8, 1, 32), (80, 16, 8, 1, 128), (80, 8, 8, 12, 64),     # 4
+                                                (80, 16, 8, 4, 64), (75, 8, 8, 16, 32)])
+def test_few_rows_of_many_heads(contexts, B, heads, kv, n, group):
+    """From two heads per SM on a CTA of the few-row kernel takes several heads, and fewer slices of the keys."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert B * kv >= 2 * sms
+    ctx = contexts(heads, 128, "bf16", max_batch=80, max_len=256)
+    rng = np.random.default_rng(B + n)
+    L = 200
+    lens = rng.integers(0, L + 1, B)
+    lens[:6] = [L, 0, 1, 32, 33, 127]
+    kc, vc = (Q.quantize(_draw(rng, (B, L, kv, 128), "bf16"), group) for _ in range(2))
+    q = Q.store(rng.standard_normal((B, n, heads, 128)), "bf16")
+    cache = _cache(B, L + 3, kv, 128, group)
+    _load(cache, kc, vc)
+    for b in range(B):
+        cache.k_scales[b, lens[b]:] = float("nan")
+        cache.v_scales[b, lens[b]:] = float("nan")
+    got = _attend(ctx, q, cache, L, lens, "bf16")
+    want, tol = Q.attention(q, Q.values(*kc, "bf16"), Q.values(*vc, "bf16"), lens, "bf16")
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= tol).all()
+
+
+@pytest.mark.parametrize("heads,hd,group", [(2, 128, 128), (2, 96, 32), (4, 64, 64)])
+def test_float32_attention_of_many_rows_over_many_keys(contexts, heads, hd, group):
+    """After a float32 context whose head_dim the cache does not take was made."""
+    ctx = contexts(heads, hd, "f32")
+    contexts(2, 48, "f32", max_batch=2, max_len=64)
+    rng = np.random.default_rng(hd)
+    B, n, L, lens = 2, 301, 1000, [1000, 897]
+    kc, vc = (Q.quantize(_draw(rng, (B, L, heads, hd), "f32"), group) for _ in range(2))
+    q = Q.store(rng.standard_normal((B, n, heads, hd)), "f32")
+    cache = _cache(B, L, heads, hd, group)
+    _load(cache, kc, vc)
+    got = _attend(ctx, q, cache, L, lens, "f32")
+    want, tol = Q.attention(q, Q.values(*kc, "f32"), Q.values(*vc, "f32"), lens, "f32")
+    assert (np.abs(got - want) <= tol).all()
+
+
+def test_rows_past_2_31_words_are_the_rows_of_a_small_cache(contexts):
+    import token_skipping_sparse_step_b200 as esd
+    ctx = contexts(16, 128, "bf16", max_batch=80, max_len=128)
+    B, cap = 80, 110000
+    words = lambda: torch.empty(B, cap, 16, 16, dtype=torch.int32, device="cuda")
+    scales = lambda: torch.empty(B, cap, 16, 1, 2, dtype=torch.bfloat16, device="cuda")
+    cache, near = esd.KVQuant(words(), words(), scales(), scales(), 128), _cache(B, 1, 16, 128, 128)
+    assert cache.k_codes[:-1].numel() > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k, v = (torch.randn(B, 2048, generator=g, device="cuda").bfloat16() for _ in range(2))
+    ctx.kv_quantize(k, v, torch.full((B, 1), cap - 1, dtype=torch.int32, device="cuda"), B, 1, cache)
+    ctx.kv_quantize(k, v, None, B, 1, near)
+    for a, b in ((cache.k_codes, near.k_codes), (cache.v_codes, near.v_codes), (cache.k_scales, near.k_scales), (cache.v_scales, near.v_scales)):
+        assert torch.equal(a[:, -1], b[:, 0])
+    out = [torch.empty(B, 2048, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    ctx.kv_dequantize(cache, torch.full((B, 1), cap - 1, dtype=torch.int32, device="cuda"), B, 1, *out[:2])
+    ctx.kv_dequantize(near, None, B, 1, *out[2:])
+    ctx.sync_check()
+    assert torch.equal(out[0], out[2]) and torch.equal(out[1], out[3]) and not torch.equal(out[0], out[1])
