@@ -343,23 +343,26 @@ typedef struct {
 /* Write rows into the 4-bit cache: row b*n + j of k and v ([B*n, n_kv_heads *
  * head_dim], storage type, RoPE already applied to k) goes to position
  * idx[b, j] of sequence b (int32 [B, n]; NULL: position j, n <= capacity).
- * A negative entry marks a padding row, of which nothing is written; entries
- * of a sequence are distinct (a position given twice holds either row, or
- * heads of both). Per group with extremes lo and hi, in float32 steps:
+ * A negative entry marks a padding row, of which nothing is written; the other
+ * entries of a sequence are distinct (what a position given twice holds is not
+ * said: codes and steps may come from different rows). Per group with extremes lo and hi, in float32 steps:
  *   t = (hi - lo) / 15,  z = lo - 16 t rounded down to bf16,
  *   s = (hi - z) / 31 rounded to bf16,
  *   c = the whole number nearest to (x - (16 s + z)) / s (the quotient exact,
  *       ties to even), clamped to 0..15; 0 where s is 0.
- * A group that holds a NaN or an infinity, or whose span overflows, gets
- * s = z = NaN and reads back as NaN. Rows that the call does not name stay as
+ * A group that holds a NaN or an infinity, or whose span, z or s overflows (z
+ * lies a span below lo: extremes of +-1.2e38 do), gets s = z = NaN and reads
+ * back as NaN. Rows that the call does not name stay as
  * they are. A position at or past the capacity is skipped and reported as
  * ESD_ERR_CHECK by the next esd_sync_check. Requires B <= max_batch,
- * 1 <= n <= max_len; k and v 16-byte aligned, apart from the cache. */
+ * 1 <= n <= max_len; k and v 16-byte aligned, apart from the cache, whose four
+ * arrays are apart from one another. */
 esd_status esd_kv_quantize(esd_ctx* ctx, const void* k, const void* v, const int32_t* idx, int B,
                            int n, const esd_kv_quant* cache, void* stream);
 
 /* Read rows of the 4-bit cache back: k_out and v_out [B*n, n_kv_heads *
- * head_dim] (storage type, 16-byte aligned), positions as for esd_kv_quantize.
+ * head_dim] (storage type, 16-byte aligned, apart from one another and from the
+ * cache), positions as for esd_kv_quantize, the same one as often as wanted.
  * The rows of negative or out-of-range positions are zeros (the latter also
  * reported as ESD_ERR_CHECK by the next esd_sync_check). */
 esd_status esd_kv_dequantize(esd_ctx* ctx, const esd_kv_quant* cache, const int32_t* idx, int B,

@@ -218,3 +218,51 @@ def test_rows_past_2_31_words_are_the_rows_of_a_small_cache(contexts):
     ctx.kv_dequantize(near, None, B, 1, *out[2:])
     ctx.sync_check()
     assert torch.equal(out[0], out[2]) and torch.equal(out[1], out[3]) and not torch.equal(out[0], out[1])
+
+
+@pytest.mark.parametrize("dtype,n", [("bf16", 4), ("bf16", 12), ("bf16", 24), ("bf16", 40), ("bf16", 100), ("bf16", 300), ("f32", 40)])
+def test_query_rows_that_are_not_finite_stay_to_themselves(contexts, dtype, n):
+    """NaN in a row, and infinite scores of both signs (softmax of +infinity: NaN); more rows than keys, too."""
+    ctx = contexts(4, 128, dtype)
+    rng = np.random.default_rng(n)
+    B, L, lens = 2, 200, [200, 33]
+    kc, vc = (Q.quantize(_draw(rng, (B, L, 4, 128), dtype), 64) for _ in range(2))
+    kk, vv = Q.values(*kc, dtype), Q.values(*vc, dtype)
+    for b in range(B):
+        for h in range(4):
+            assert (kk[b, :lens[b], h, 9] > 0).any() and (kk[b, :lens[b], h, 9] < 0).any()
+    q = Q.store(rng.standard_normal((B, n, 4, 128)), dtype)
+    hit = np.zeros((B, n, 4), bool)
+    hit[0, 1, 2] = hit[1, n - 1, 0] = True
+    q[0, 1, 2, 100], q[1, n - 1, 0, 9] = np.nan, np.inf
+    cache = _cache(B, L, 4, 128, 64)
+    _load(cache, kc, vc)
+    got = _attend(ctx, q, cache, L, lens, dtype)
+    want, tol = Q.attention(np.where(hit[..., None], 0.0, q), kk, vv, lens, dtype)
+    assert np.array_equal(np.isnan(got), np.broadcast_to(hit[..., None], got.shape))
+    assert (np.abs(got - want) <= tol)[~hit].all()
+
+
+@pytest.mark.parametrize("dtype,heads,hd,group", [("bf16", 4, 128, 32), ("bf16", 4, 128, 128), ("f32", 2, 64, 64)])
+def test_a_position_given_twice_leaves_the_others_right(contexts, dtype, heads, hd, group):
+    """What that position itself holds is not said: its codes and steps may come from either row."""
+    ctx = contexts(heads, hd, dtype)
+    rng = np.random.default_rng(hd)
+    n, cap = 300, 400
+    k, v = (_draw(rng, (1, n, heads, hd), dtype) for _ in range(2))
+    idx = rng.permutation(cap)[:n].astype(np.int32)
+    twice = [int(idx[i]) for i in (0, 7, 290)]
+    idx[[150, 8, 299]] = twice
+    cache = _cache(1, cap, heads, hd, group)
+    ctx.kv_quantize(*(to_gpu(x.reshape(n, -1), DT[dtype]) for x in (k, v)), to_gpu(idx[None], torch.int32), 1, n, cache)
+    out = [torch.empty(n, heads * hd, dtype=DT[dtype], device="cuda") for _ in range(2)]
+    ctx.kv_dequantize(cache, to_gpu(idx[None], torch.int32), 1, n, *out)
+    ctx.sync_check()
+    alone = ~np.isin(idx, twice)
+    assert alone.sum() == n - 6
+    for x, o in ((k, out[0]), (v, out[1])):
+        back = o.float().cpu().numpy().astype(np.float64).reshape(n, heads, hd)
+        assert np.array_equal(back[alone], Q.values(*Q.quantize(x, group), dtype)[0][alone]) and np.isfinite(back).all()
+    named = torch.zeros(cap, dtype=torch.bool)
+    named[torch.from_numpy(idx).long()] = True
+    assert not cache.k_scales[0][~named.cuda()].any() and not cache.v_codes[0][~named.cuda()].any()
