@@ -38,7 +38,10 @@
 //
 // The running maximum moves only when a chunk's exceeds it by more than 2^8 (O is
 // then scaled in TMEM; the result O / l is the same). P is rounded to bf16 for its
-// product, everything else is float32. Keys at or past the sequence's length are
+// product, everything else is float32: both operands of an MMA have one type, V's
+// values are bf16 (their range leaves no other type of 16 bits), and P in two parts
+// would double the product; it moves an output by at most 2^-8 of sum p |v|, the size
+// of the output's own rounding. Keys at or past the sequence's length are
 // masked, and read as zeros. The slices of a row tile are the CTAs of a cluster,
 // merged through distributed shared memory in slice order. Every mbarrier wait is
 // bounded (error flag); every CTA reaches every cluster barrier.
