@@ -1,6 +1,10 @@
 """Edges of the 4-bit key/value cache on the GPU: groups whose grid float32 cannot
 resolve, scores that are infinite, calls on one stream without a wait between
 them, and the few-row kernel with several heads to a CTA."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -266,3 +270,51 @@ def test_a_position_given_twice_leaves_the_others_right(contexts, dtype, heads, 
     named = torch.zeros(cap, dtype=torch.bool)
     named[torch.from_numpy(idx).long()] = True
     assert not cache.k_scales[0][~named.cuda()].any() and not cache.v_codes[0][~named.cuda()].any()
+
+
+FIRST = r"""
+import sys
+sys.path.insert(0, %r)
+import torch
+import token_skipping_sparse_step_b200 as esd
+n, share = int(sys.argv[1]), int(sys.argv[2])
+B, L, kv, group, d = 2, 3239, 28 // share, 32, 28 * 128
+new = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+layer = {"wq": new(d, d), "wk": new(d, d), "wv": new(d, d), "wo": new(d, d), "wg": new(128, d), "wu": new(128, d), "wd": new(d, 128)}
+ctx = esd.Context(esd.make_dims(2, d, 28, 128, 128, 128, 127, dtype="bf16"), {"embed": new(128, d), "w_out": new(128, d), "layers": [layer, layer]},
+                  esd.make_run(skip_layer=1, max_batch=B, max_len=L))
+g = torch.Generator(device="cuda").manual_seed(n)
+rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+cache = esd.KVQuant.empty(B, L, kv, 128, group)
+k, v, q = rnd(B * L, kv * 128), rnd(B * L, kv * 128), rnd(B * n, 28 * 128)
+ctx.kv_quantize(k * 2, v, None, B, L, cache)
+ctx.kv_dequantize(cache, None, B, L, k, v)
+lens = torch.tensor([L, 2744], dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+outs = [torch.empty_like(q) for _ in range(6)]
+for o in outs:              # the first of them is the kernel's first launch in this process
+    ctx.partial_attention_quantized(q, cache, B, L, n, o, lens=lens)
+ctx.sync_check()
+assert all(torch.equal(outs[0], o) for o in outs[1:]), "not the same bits each time"
+# bf16: P and the output are rounded, 2^-8 each; float32 sums as in kvq_oracle.attention
+u, e = 2.0 ** -8, 2.0 ** -24
+for b in range(B):
+    for h in range(28):
+        m = int(lens[b])
+        kk = k.view(B, L, kv, 128)[b, :m, h // share].double()
+        vv = v.view(B, L, kv, 128)[b, :m, h // share].double()
+        qq = q.view(B, n, 28, 128)[b, :, h].double()
+        p = torch.softmax(qq @ kk.T / 128 ** 0.5, -1)
+        want, a = p @ vv, p @ vv.abs()
+        size = 1 + (qq.abs() @ kk.abs().T / 128 ** 0.5).amax(-1, keepdim=True)
+        tol = u * want.abs() + u * a + 2 * (136 * size + m + 16) * e * a
+        assert ((outs[0].view(B, n, 28, 128)[b, :, h].double() - want).abs() <= tol).all(), (b, h)
+"""
+
+
+@pytest.mark.parametrize("n,share", [(88, 1), (40, 1), (24, 1), (200, 1), (9, 1)])
+def test_the_first_launch_of_a_process(n, share):
+    """Caches of instructions, addresses and data are cold, and warps and copies come at other times than ever after."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST % root, str(n), str(share)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

@@ -37,9 +37,9 @@ WALK = r"""
 #include <cstdlib>
 #include <set>
 #include <algorithm>
-// The walk of the expanding warps: K of chunk j + 1 is waited for, its stage may not come free, then V of chunk j is
-// read, which frees the chunk's ring stage for the copy of chunk j + stages, and its stage may not come free. It gives
-// up at its wait number `at`. Prints what is in flight then, and what is drained.
+// The walk of the expanding warps: K of chunk j + 1 is waited for, its stage may not come free, nor V's of chunk j;
+// when both are expanded, the chunk's ring stage takes the copy of chunk j + stages. It gives up at its wait number
+// `at`. Prints what is in flight then, and what is drained.
 int main(int argc, char** argv) {
   const int nc = atoi(argv[1]), stages = atoi(argv[2]), at = atoi(argv[3]);
   esd::CopyWindow w;
@@ -57,8 +57,8 @@ int main(int argc, char** argv) {
       if (j + 1 >= 2 && !(ok = wait())) break;
     }
     if (j >= 0) {
-      if (j + stages < nc) copy(j + stages);
       if (j >= 2 && !(ok = wait())) break;
+      if (j + stages < nc) copy(j + stages);
     }
   }
   printf("%d\n", (int)ok);
@@ -124,3 +124,15 @@ def test_a_cache_on_another_device_than_the_context_is_refused(device):
     else:
         with pytest.raises(ValueError, match="context"):
             ctx._check_rows(cache, 2, "k, v", 100, rows, rows, (None, 8))
+
+
+def test_a_ring_stage_is_refilled_only_when_what_was_read_of_it_is_written():
+    """A copy (asynchronous proxy) is not ordered behind loads whose values nobody has used yet."""
+    code = _code("attention_quant_tc.cuh")
+    step = code[code.index("auto step = [&]"):]
+    step = step[:step.index("constexpr int kSc")]
+    reads, written, refill = step.rindex("lds128("), step.index("expand(aV"), step.index("copy(j + kStages)")
+    assert reads < written < refill
+    expand = code[code.index("auto expand = [&]"):]
+    expand = expand[:expand.index("bool ok = true")]
+    assert expand.index("sts128(") < expand.index("fence.proxy.async.shared::cta") < expand.index("__syncwarp()")

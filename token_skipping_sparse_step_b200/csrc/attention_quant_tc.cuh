@@ -277,12 +277,17 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
       if (j >= 0) {
         const int rs = j % kStages, st = j & 1;
         const uint4 c[2] = {lds128(src + rs * 2048 + 1024), lds128(src + rs * 2048 + 1536)};
-        __syncwarp();
-        if (lane == 0 && j + kStages < nc) copy(j + kStages);  // the stage has been read
         if (j >= 2) ok = warp_wait(vempty + 8 * st, (uint32_t)(((j >> 1) - 1) & 1), abort_flag, flag);
         if (!ok) return;
         expand(aV + st * kAtTile, c, av.v, len - (c0 + j) * kAtKeys);
-        if (lane == 0) mbar_arrive(vfull + 8 * st);
+        if (lane == 0) {
+          mbar_arrive(vfull + 8 * st);
+          // Only here has the stage been read: the tiles hold what the loads above brought, behind the fence that ends
+          // expand(). A copy does not queue behind loads that are on their way, and could overtake them: issued before
+          // the wait, it gave some keys of a head the values of a later chunk in 2 of 3 first launches of a process
+          // (88 rows x 3239 keys). Nor is it late here (16 x 1024 rows x 4096 keys: 1567 -> 1549 us, the others the same)
+          if (j + kStages < nc) copy(j + kStages);
+        }
       }
     };
     constexpr int kSc = 4;  // chunks of steps and offsets in registers
