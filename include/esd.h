@@ -318,8 +318,10 @@ esd_status esd_partial_attention(esd_ctx* ctx, const void* q, const void* k_cach
 
 /* Key/value cache in 4 bits (no counterpart in the papers: it holds the K and V
  * of the partial cache in about a quarter of the bytes, for long contexts and
- * large batches). Memory of the context's device, owned by the caller, 16-byte
- * aligned:
+ * large batches). Memory of the context's device, owned by the caller; codes
+ * 16-byte aligned, scales to the pairs of a head (4, 8 or 16 bytes for 1, 2 or 4
+ * groups a head, 4 for 3), so that a layer of one array over all layers is
+ * aligned whatever its sizes:
  *  k_codes, v_codes   uint32 [B, capacity, n_kv_heads, head_dim / 8]: 4-bit
  *    codes, dim 2i of a word's eight in bits 4i..4i+3, dim 2i+1 in bits
  *    16+4i..16+4i+3;

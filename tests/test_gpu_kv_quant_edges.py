@@ -318,3 +318,34 @@ def test_the_first_launch_of_a_process(n, share):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST % root, str(n), str(share)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("dtype,heads,hd,group", [("bf16", 1, 128, 128), ("bf16", 3, 128, 64), ("bf16", 3, 128, 32), ("f32", 3, 32, 32),
+                                                  ("f32", 1, 96, 32), ("f32", 3, 128, 64)])
+def test_a_layer_of_one_array_over_all_layers(contexts, dtype, heads, hd, group):
+    """Views whose steps and offsets start at a head's pairs, not at 16 bytes: the bits of a cache of its own."""
+    import token_skipping_sparse_step_b200 as esd
+    ctx = contexts(heads, hd, dtype)
+    g = torch.Generator(device="cuda").manual_seed(hd)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(DT[dtype])
+    B, cap, L = 1, 331, 317
+    codes = torch.zeros(2, 4, B, cap, heads, hd // 8, dtype=torch.int32, device="cuda")
+    scales = torch.zeros(2, 4, B, cap, heads, hd // group, 2, dtype=torch.bfloat16, device="cuda")
+    assert (hd, group) == (128, 32) or any(t.data_ptr() % 16 for t in scales.flatten(0, 1))
+    k, v, idx = rnd(L, heads * hd), rnd(L, heads * hd), torch.arange(L, device="cuda", dtype=torch.int32)[None].contiguous()
+    q = rnd(200, heads * hd)
+    want = None
+    for layer in (None, 0, 1, 2, 3):
+        cache = _cache(B, cap, heads, hd, group) if layer is None else esd.KVQuant(codes[0, layer], codes[1, layer], scales[0, layer], scales[1, layer], hd)
+        ctx.kv_quantize(k, v, idx, B, L, cache)
+        back = [torch.empty_like(k) for _ in range(2)]
+        ctx.kv_dequantize(cache, idx, B, L, *back)
+        outs = []
+        for n in (1, 12, 24, 50, 100, 200):
+            outs.append(torch.empty_like(q[:n]))
+            ctx.partial_attention_quantized(q[:n], cache, B, L, n, outs[-1])
+        ctx.sync_check()
+        got = [cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales, *back, *outs]
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.isfinite(want[-1]).all() and want[-1].any()

@@ -573,11 +573,14 @@ esd_status check_kv(esd_ctx* c, const esd_kv_quant* kv, esd::KvQuant* out) {
     return fail(c, ESD_ERR_INVALID_ARG, "null pointer");
   const uintptr_t codes = (uintptr_t)kv->k_codes | (uintptr_t)kv->v_codes;
   const uintptr_t scales = (uintptr_t)kv->k_scales | (uintptr_t)kv->v_scales;
-  if ((codes & 15) || (scales & 15)) return fail(c, ESD_ERR_INVALID_ARG, "cache pointers need 16-byte alignment");
+  if (codes & 15) return fail(c, ESD_ERR_INVALID_ARG, "the codes need 16-byte alignment");
   const int H = c->dims.n_heads, hd = c->dims.head_dim, g = kv->group;
   if (g != 32 && g != 64 && g != 128) return fail(c, ESD_ERR_INVALID_ARG, "group %d is not 32, 64 or 128", g);
   if (hd % 32) return fail(c, ESD_ERR_UNSUPPORTED, "head_dim %d is not a multiple of 32", hd);
   if (hd % g) return fail(c, ESD_ERR_INVALID_ARG, "group %d does not divide head_dim %d", g, hd);
+  // the few-row attention copies a head's 1, 2 or 4 pairs at once; a head of 3 is read pair by pair
+  const uintptr_t pairs = 4u * (uintptr_t)(hd / g & -(hd / g));
+  if (scales & (pairs - 1)) return fail(c, ESD_ERR_INVALID_ARG, "steps and offsets need %d-byte alignment", (int)pairs);
   if (kv->n_kv_heads < 1 || H % kv->n_kv_heads)
     return fail(c, ESD_ERR_INVALID_ARG, "%d key/value heads do not divide %d heads", kv->n_kv_heads, H);
   if (kv->capacity < 1) return fail(c, ESD_ERR_INVALID_ARG, "capacity %d", kv->capacity);
