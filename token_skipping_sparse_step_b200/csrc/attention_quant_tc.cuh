@@ -29,9 +29,9 @@
 // stores are free of bank conflicts. Without copies the softmax warps take registers
 // from these (setmaxnreg).
 //
-// What bounds it: that chain. 16 x 1024 rows x 4096 keys x 32 heads take 1566 us (702
+// What bounds it: that chain. 16 x 1024 rows x 4096 keys x 32 heads take 1549 us (710
 // TFLOP/s), 15% less without exponentials, 22% less without products, the same
-// without the expansion; 32 x 64 rows x 6144 keys 1.4 us per 128 keys and CTA, 1.15
+// without the expansion (the tensor pipe is active 32% of the cycles); 32 x 64 rows x 6144 keys 1.4 us per 128 keys and CTA, 1.15
 // with every load, expansion and product taken out. A CTA's start and merge cost
 // about 7 us, which shows where each has few chunks (32 x 64 rows x up to 1536 keys:
 // 135 us).

@@ -144,8 +144,10 @@ __device__ __forceinline__ int kv_row_of(int i, uint32_t magic) { return (int)__
 // the bottom of the range, whose own rounding is coarse (and which are scaled to keep
 // their reciprocal finite). What bounds it is the
 // instructions, about 20 a value at 3.3 of the 4 that an SM can issue: 16 x 4096 rows
-// of 32 heads take 339 us (1.37 GB, 4.0 TB/s). Two values to an instruction where
-// there is one for a pair took 605 to 561 us with the reading back.
+// of 32 heads take 338 us (1.38 GB, 4.1 TB/s). Two values to an instruction where
+// there is one for a pair took 605 to 561 us with the reading back. float32 rows are
+// bound by their bytes: 8 x 2048 rows of 16 heads 51.6 us (5.9 TB/s), 0.7 of it the
+// clamp.
 // ---------------------------------------------------------------------------
 template <typename T>
 __device__ __forceinline__ void kv_load16(const T* p, float (&x)[16], float& lo, float& hi) {
@@ -267,7 +269,8 @@ kv_quantize_kernel(const T* k, const T* v, const int32_t* idx, int rows, int n,
 // Rows of the cache back into k_out, v_out [B n, n_kv hd] (storage type); zeros
 // for a padding row. An item is one word (8 values); a thread has four in flight (one
 // at a time: 356 us for 222). Bound by the bytes, most of them written: 16 x 4096
-// rows of 32 heads, groups of 128, 222 us, 6.1 TB/s.
+// rows of 32 heads, groups of 128, 222 us, 6.1 TB/s; 8 x 2048 float32 rows of 16
+// heads 63.5 us, 4.8 TB/s.
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(kKvThreads)
