@@ -136,3 +136,10 @@ def test_a_ring_stage_is_refilled_only_when_what_was_read_of_it_is_written():
     expand = code[code.index("auto expand = [&]"):]
     expand = expand[:expand.index("bool ok = true")]
     assert expand.index("sts128(") < expand.index("fence.proxy.async.shared::cta") < expand.index("__syncwarp()")
+
+
+def test_the_barriers_of_the_first_copies_are_fenced_for_them():
+    """They are started by the thread that set the barriers up, ahead of any barrier of the block."""
+    code = _code("attention_quant_tc.cuh")
+    init, first = code.index("mbar_init(rawfull"), code.index("min(kStages, nc); ++j) copy(j)")
+    assert init < code.index("fence.proxy.async.shared::cta", init) < first

@@ -178,6 +178,8 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_
   if (warp >= 8 && lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(rawfull + ((warp - 8) * kStages + i) * 8, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    // the copies, which no barrier of the block follows first, see them too
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     for (int j = 0; j < min(kStages, nc); ++j) copy(j);
   }
   auto row_at = [&](int i) {  // of Q and O
