@@ -349,3 +349,45 @@ def test_a_layer_of_one_array_over_all_layers(contexts, dtype, heads, hd, group)
         want = want or got
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert torch.isfinite(want[-1]).all() and want[-1].any()
+
+
+@pytest.mark.parametrize("dtype,hd", [("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("seed", [0, 1])
+def test_calls_in_any_order_without_a_wait(contexts, dtype, hd, seed):
+    """Writes, reads, and attention of one to many rows over long and short sequences, on one stream, two caches and
+    shared outputs: the bits of the same calls with a wait after each."""
+    ctx = contexts(4, hd, dtype, max_batch=2, max_len=3000)
+    d = 4 * hd
+    results = []
+    for wait in (True, False):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(DT[dtype])
+        rng = np.random.default_rng(seed)
+        B, cap = 2, 3000
+        caches = [_cache(B, cap, kv, hd, 32) for kv in (4, 2)]
+        pool = [rnd(B * cap, d) for _ in range(3)]
+        kept = []
+        torch.cuda.synchronize()
+        for c in caches:
+            ctx.kv_quantize(pool[0], pool[1], None, B, cap, c)
+        for _ in range(60):
+            c = caches[rng.integers(2)]
+            n = int(rng.choice([1, 2, 9, 24, 40, 88, 128, 150, 300]))
+            idx = to_gpu(np.stack([rng.permutation(cap)[:n] for _ in range(B)]).astype(np.int32), torch.int32)
+            lens = to_gpu(rng.integers(0, cap + 1, B).astype(np.int32), torch.int32)
+            a, b, o = (pool[i] for i in rng.permutation(3))
+            kind = rng.integers(4)
+            if kind == 0:
+                ctx.kv_quantize(a, b, idx, B, n, c)
+            elif kind == 1:
+                ctx.kv_dequantize(c, idx, B, n, a, b)
+            else:
+                ctx.partial_attention_quantized(a, c, B, cap, n, o, lens=None if kind == 2 else lens)
+                kept.append(o[:B * n].clone())
+            if wait:
+                torch.cuda.synchronize()
+        ctx.sync_check()
+        results.append([*kept, *pool, *(t for c in caches for t in (c.k_codes, c.v_codes, c.k_scales, c.v_scales))])
+    assert len(kept) > 15
+    for x, y in zip(*results):
+        assert torch.equal(torch.nan_to_num(x), torch.nan_to_num(y))
