@@ -347,15 +347,15 @@ typedef struct {
  * idx[b, j] of sequence b (int32 [B, n]; NULL: position j, n <= capacity).
  * A negative entry marks a padding row, of which nothing is written; the other
  * entries of a sequence are distinct (what a position given twice holds is not
- * said: codes and steps may come from different rows). Per group with extremes lo and hi, in float32 steps:
+ * said: codes and steps may come from different rows). Per group with extremes
+ * lo and hi, in float32 steps:
  *   t = (hi - lo) / 15,  z = lo - 16 t rounded down to bf16,
  *   s = (hi - z) / 31 rounded to bf16,
  *   c = the whole number nearest to (x - (16 s + z)) / s (the quotient exact,
  *       ties to even), clamped to 0..15; 0 where s is 0.
  * A group that holds a NaN or an infinity, or whose span, z or s overflows (z
  * lies a span below lo: extremes of +-1.2e38 do), gets s = z = NaN and reads
- * back as NaN. Rows that the call does not name stay as
- * they are. A position at or past the capacity is skipped and reported as
+ * back as NaN. Rows that the call does not name stay as they are. A position at or past the capacity is skipped and reported as
  * ESD_ERR_CHECK by the next esd_sync_check. Requires B <= max_batch,
  * 1 <= n <= max_len; k and v 16-byte aligned, apart from the cache, whose four
  * arrays are apart from one another. */
@@ -376,8 +376,8 @@ esd_status esd_kv_dequantize(esd_ctx* ctx, const esd_kv_quant* cache, const int3
  * be NULL): sequence b has min(lens[b], L) keys; rows behind them are not
  * attended to, whatever the cache holds there, and the outputs of a sequence
  * without keys are zeros. A row whose scores are all -infinity (an infinite
- * query) is NaN, as in esd_partial_attention. q, out: [B*k, d] (RoPE already applied to q), 16-byte
- * aligned, not overlapping. Requires B <= max_batch, 1 <= L <= max_len,
+ * query) is NaN, as in esd_partial_attention. q, out: [B*k, d] (RoPE already
+ * applied to q), 16-byte aligned, not overlapping. Requires B <= max_batch, 1 <= L <= max_len,
  * L <= capacity, 1 <= k <= max_len. */
 esd_status esd_partial_attention_quantized(esd_ctx* ctx, const void* q, const esd_kv_quant* cache,
                                            const int32_t* lens, int B, int L, int k, void* out,

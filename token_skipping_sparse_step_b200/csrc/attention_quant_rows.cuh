@@ -24,7 +24,7 @@
 // operands of the product have one type, V's values are bf16 already (their range
 // leaves no other type of 16 bits), and P kept to more bits would take a second
 // product per tile. It moves an output by at most 2^-8 of sum p |v|, the size of its
-// own rounding; measured 0.0018 to 0.0023 from 64 bits, where float32 P has 0.0017.
+// own rounding; measured 0.0019 to 0.0024 from 64 bits, where float32 P has 0.0017.
 //
 // Each warp copies its own blocks (cp.async, no other thread waits on them)
 // through a ring of its own in shared memory; two rows of codes share a 128-byte
@@ -33,7 +33,7 @@
 // ahead) took 78 us where this takes 61 to 66: its addresses and its registers
 // cost the occupancy that hides the latency.
 //
-// What bounds it: 32 sequences x 1536 keys x 32 heads, groups of 64, one row: 66 us,
+// What bounds it: 32 sequences x 1536 keys x 32 heads, groups of 64, one row: 67 us,
 // 3.4 TB/s of the 226 MB (a bare copy of those codes in one launch, 64 bytes a row
 // and head, reaches 4.5 TB/s). The bit operations of the expansion (two per pair of
 // values, at half the issue rate) keep their pipe at 55%; shifts taken as products,

@@ -31,10 +31,10 @@
 //
 // What bounds it: that chain. 16 x 1024 rows x 4096 keys x 32 heads take 1549 us (710
 // TFLOP/s), 15% less without exponentials, 22% less without products, the same
-// without the expansion (the tensor pipe is active 32% of the cycles); 32 x 64 rows x 6144 keys 1.4 us per 128 keys and CTA, 1.15
-// with every load, expansion and product taken out. A CTA's start and merge cost
-// about 7 us, which shows where each has few chunks (32 x 64 rows x up to 1536 keys:
-// 135 us).
+// without the expansion (the tensor pipe is active 32% of the cycles); 32 x 64 rows x
+// 6144 keys 1.4 us per 128 keys and CTA, 1.15 with every load, expansion and product
+// taken out. A CTA's start and merge cost about 7 us, which shows where each has few
+// chunks (32 x 64 rows x up to 1536 keys: 135 us).
 //
 // The running maximum moves only when a chunk's exceeds it by more than 2^8 (O is
 // then scaled in TMEM; the result O / l is the same). P is rounded to bf16 for its
